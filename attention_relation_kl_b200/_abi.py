@@ -22,7 +22,8 @@ EXPORTS = ("relkl_workspace_bytes", "relkl_workspace_init", "relkl_fwd", "relkl_
            "relkl_set_wait_timeout_ns", "relkl_status_string", "relkl_last_cuda_error",
            "relkl_path_for", "relkl_fwd_noalloc", "relkl_rope_bwd", "relkl_weight_grad",
            "relkl_cast_bf16", "relkl_bwd_kernel_for",
-           "relkl_fwd_qkv_part", "relkl_bwd_qkv_part", "relkl_check_schedule")
+           "relkl_fwd_qkv_part", "relkl_bwd_qkv_part", "relkl_check_schedule",
+           "relkl_rotary")
 
 
 class relkl_desc(ctypes.Structure):
@@ -38,6 +39,22 @@ class relkl_rope(ctypes.Structure):
     _fields_ = [("base", ctypes.c_double), ("pos_scale", ctypes.c_double),
                 ("pos_offset", ctypes.c_double), ("apply", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class relkl_rotary_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3),
+                ("H", ctypes.c_int32), ("apply", ctypes.c_int32)]
+
+
+class relkl_rotary_plan(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("x_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("positions", ctypes.c_void_p), ("pos_stride", ctypes.c_int64 * 2),
+                ("pos_bytes", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("pos_scale", ctypes.c_double), ("pos_offset", ctypes.c_double),
+                ("inv_freq", ctypes.c_void_p)]
 
 
 _vp = ctypes.c_void_p
@@ -95,6 +112,9 @@ def _declare(lib):
     lib.relkl_weight_grad.restype = ctypes.c_int
     lib.relkl_weight_grad.argtypes = [ctypes.c_int64, i32, i32, _vp, _vp, _vp, _vp,
                                       ctypes.c_size_t, _vp]
+    lib.relkl_rotary.restype = ctypes.c_int
+    lib.relkl_rotary.argtypes = [i32, ctypes.POINTER(relkl_rotary_tensor),
+                                 ctypes.POINTER(relkl_rotary_plan), _vp]
     return lib
 
 

@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include <cuda.h>
@@ -31,6 +32,8 @@ int tc_bwd_kind(const TcParams& p, int d, int sms);
 cudaError_t launch_rope_bwd(const float* dx, void* out, int B, int H, int N, int d, bool bf16_out,
                             double base, double pos_scale, double pos_offset, int apply,
                             cudaStream_t stream);
+cudaError_t launch_rotary(RotaryParams& p, bool x_bf16, bool y_bf16, bool interleaved,
+                          int num_sms, cudaStream_t stream);
 using EncodeTiledFnG = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                     const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                     const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -643,6 +646,110 @@ relkl_status relkl_rope_bwd(int32_t B, int32_t H, int32_t N, int32_t d, const fl
   cudaError_t e = launch_rope_bwd(dx_post, dx_pre, B, H, N, d, out_dtype == RELKL_BF16, rope->base,
                                   rope->pos_scale, rope->pos_offset, rope->apply,
                                   static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
+}
+
+relkl_status relkl_rotary(int32_t n_tensors, const relkl_rotary_tensor* tensors,
+                          const relkl_rotary_plan* plan, void* stream) {
+  NvtxRange nvtx_range("relkl_rotary");
+  if (n_tensors < 1 || n_tensors > kMaxSeg || !tensors || !plan) return RELKL_ERR_INVALID;
+  const relkl_rotary_plan& a = *plan;
+  if (a.B < 0 || a.N < 0 || a.d < 1 || a.d > 512 || a.rot < 0 || a.rot > a.d || (a.rot & 1))
+    return RELKL_ERR_INVALID;
+  if ((a.x_dtype != RELKL_BF16 && a.x_dtype != RELKL_FP32) ||
+      (a.y_dtype != RELKL_BF16 && a.y_dtype != RELKL_FP32))
+    return RELKL_ERR_INVALID;
+  if ((a.interleaved != 0 && a.interleaved != 1) || (a.inverse != 0 && a.inverse != 1))
+    return RELKL_ERR_INVALID;
+  if (!std::isfinite(a.pos_scale) || !std::isfinite(a.pos_offset) || !std::isfinite(a.mscale))
+    return RELKL_ERR_INVALID;
+  if (a.positions) {
+    if ((a.pos_bytes != 4 && a.pos_bytes != 8) || !aligned(a.positions, a.pos_bytes) ||
+        a.pos_stride[0] < 0 || a.pos_stride[1] < 0)
+      return RELKL_ERR_INVALID;
+  } else if (a.pos_bytes != 0) {
+    return RELKL_ERR_INVALID;
+  }
+  const int64_t xs = a.x_dtype == RELKL_BF16 ? 2 : 4, ys = a.y_dtype == RELKL_BF16 ? 2 : 4;
+  RotaryParams p;
+  std::memset(&p, 0, sizeof(p));
+  struct Range { const char *x0, *x1, *y0, *y1; bool in_place; } range[kMaxSeg];
+  bool turns = false;
+  for (int r = 0; r < n_tensors; ++r) {
+    const relkl_rotary_tensor& t = tensors[r];
+    if (t.H < 0 || (t.apply != 0 && t.apply != 1)) return RELKL_ERR_INVALID;
+    if (t.H == 0 || a.B == 0 || a.N == 0) continue;
+    if (!t.x || !t.y || !aligned(t.x, xs) || !aligned(t.y, ys)) return RELKL_ERR_INVALID;
+    const int64_t extent[3] = {a.B, t.H, a.N};
+    RotaryTensor& k = p.t[p.n];
+    k.x = t.x;
+    k.y = t.y;
+    k.H = t.H;
+    k.apply = t.apply && a.rot > 0;
+    turns = turns || k.apply;
+    bool same = t.x == t.y && a.x_dtype == a.y_dtype;
+    int64_t x_span = a.d, y_span = a.d;   // elements from the first to behind the last
+    for (int i = 0; i < 3; ++i) {
+      // a dimension of extent 1 may carry any stride; the bound keeps every
+      // offset below 2^62 bytes
+      k.xs[i] = extent[i] > 1 ? t.x_stride[i] : 0;
+      k.ys[i] = extent[i] > 1 ? t.y_stride[i] : 0;
+      if (k.xs[i] < 0 || k.ys[i] < 0 || k.xs[i] > (int64_t(1) << 48) / extent[i] ||
+          k.ys[i] > (int64_t(1) << 48) / extent[i])
+        return RELKL_ERR_INVALID;
+      same = same && k.xs[i] == k.ys[i];
+      x_span += (extent[i] - 1) * k.xs[i];
+      y_span += (extent[i] - 1) * k.ys[i];
+    }
+    // y's elements are distinct: by growing stride, each step passes all that
+    // the smaller ones reach
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 2 - i; ++j)
+        if (k.ys[order[j]] > k.ys[order[j + 1]]) std::swap(order[j], order[j + 1]);
+    int64_t reach = a.d;
+    for (int i = 0; i < 3; ++i) {
+      const int o = order[i];
+      if (extent[o] == 1) continue;
+      if (k.ys[o] < reach) return RELKL_ERR_INVALID;
+      reach += (extent[o] - 1) * k.ys[o];
+    }
+    Range& g = range[p.n];
+    g.x0 = static_cast<const char*>(t.x);
+    g.x1 = g.x0 + x_span * xs;
+    g.y0 = static_cast<const char*>(t.y);
+    g.y1 = g.y0 + y_span * ys;
+    g.in_place = same;
+    ++p.n;
+  }
+  if (p.n == 0) return RELKL_OK;
+  // Tensors that are parts of one buffer interleave their ranges, so ranges
+  // are held against each other only where an x meets a y, and not where both
+  // tensors are rotated in place.
+  for (int i = 0; i < p.n; ++i)
+    for (int j = 0; j < p.n; ++j) {
+      if (range[i].in_place && range[j].in_place) continue;
+      if (range[i].x0 < range[j].y1 && range[j].y0 < range[i].x1) return RELKL_ERR_INVALID;
+    }
+  if (turns && (!a.inv_freq || !aligned(a.inv_freq, 8))) return RELKL_ERR_INVALID;
+  p.B = a.B;
+  p.N = a.N;
+  p.d = a.d;
+  p.rot = a.rot;
+  p.inv_freq = a.inv_freq;
+  p.positions = a.positions;
+  p.pos_stride[0] = a.pos_stride[0];
+  p.pos_stride[1] = a.pos_stride[1];
+  p.pos_bytes = a.pos_bytes;
+  p.inverse = a.inverse;
+  p.mscale = a.mscale;
+  p.pos_scale = a.pos_scale;
+  p.pos_offset = a.pos_offset;
+  relkl_status s;
+  DevInfo dev;
+  if ((s = device_info(&dev)) != RELKL_OK) return s;
+  cudaError_t e = launch_rotary(p, a.x_dtype == RELKL_BF16, a.y_dtype == RELKL_BF16,
+                                a.interleaved != 0, dev.sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
 }
 

@@ -76,4 +76,31 @@ struct SimtParams {
   int nblk_local;      // ceil((ceil(N / 32) - part) / n_parts)
 };
 
+// One tensor of a rotary call: element (b, h, n, k) of x at
+// x + b*xs[0] + h*xs[1] + n*xs[2] + k, of y likewise.
+struct RotaryTensor {
+  const void* x;
+  void* y;
+  int64_t xs[3], ys[3];      // element strides of B, H, N
+  int H;
+  int apply;                 // 0: moved and converted only
+  int groups;                // head groups (set by the launch)
+};
+
+struct RotaryParams {
+  RotaryTensor t[kMaxSeg];
+  int n;
+  int B, N, d, rot;
+  const double* inv_freq;    // [rot / 2] (device)
+  const void* positions;     // int32 or int64 (device), or null (0, 1, ..., N - 1)
+  int64_t pos_stride[2];
+  int pos_bytes;
+  int inverse;
+  float mscale;
+  double pos_scale, pos_offset;
+  // set by the launch
+  int chunks, rot_chunks, heads_per_group;
+  int64_t n_items;
+};
+
 }  // namespace relkl

@@ -11,6 +11,7 @@ tensors with a contiguous last dimension; kl is [B, H, N] float32, stats is
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Dict, List, Optional, Sequence, Tuple
 
@@ -83,6 +84,21 @@ def _stream(device: torch.device, stream=None) -> int:
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream=None):
+    """Makes ``device`` current, and ``stream`` (a torch stream or a cudaStream_t
+    handle) if one is given, so that what a call allocates for itself belongs to
+    the stream that uses it.  Yields the cudaStream_t handle."""
+    with contextlib.ExitStack() as st:
+        if torch.cuda.current_device() != device.index:
+            st.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            st.enter_context(torch.cuda.stream(stream))
+        yield _stream(device)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:

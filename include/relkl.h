@@ -330,6 +330,58 @@ relkl_status relkl_weight_grad(int64_t rows, int32_t D, int32_t cols, const void
                                const void* dx_pre, float* dw, void* ws, size_t ws_bytes,
                                void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions of the relation inputs, for the teacher at its own
+ * positions and the student at scaled ones, and of their gradients.
+ */
+
+/* One tensor of a relkl_rotary call: logical shape [B, H, N, d], element
+ * (b, h, n, k) of x at x + b*x_stride[0] + h*x_stride[1] + n*x_stride[2] + k
+ * (elements), of y likewise, so that a projection's token-major output can be
+ * read and a head-major relation input written by the same call.             */
+typedef struct {
+  const void* x;         /* in                                                */
+  void* y;               /* out, overwritten                                  */
+  int64_t x_stride[3], y_stride[3];
+  int32_t H;
+  int32_t apply;         /* 1: rotate (Q, K); 0: only move and convert (V)    */
+} relkl_rotary_tensor;
+
+typedef struct {
+  int32_t B, N, d;
+  int32_t rot;           /* the first rot entries of a head rotate: even, 0 <= rot <= d */
+  int32_t x_dtype, y_dtype;   /* relkl_dtype of every x and every y           */
+  int32_t interleaved;   /* 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1)    */
+  int32_t inverse;       /* 0: rotate; 1: rotate back (the gradient of 0)     */
+  /* pos(b, n) = pos_offset + pos_scale * p, p = n, or with positions != NULL
+   * positions[b*pos_stride[0] + n*pos_stride[1]] (DEVICE int32 or int64)     */
+  const void* positions;
+  int64_t pos_stride[2];
+  int32_t pos_bytes;     /* 4 or 8; 0 with positions NULL                     */
+  float mscale;          /* factor on the rotated entries, in both directions */
+  double pos_scale, pos_offset;
+  const double* inv_freq;     /* DEVICE [rot / 2]: angle of pair i = pos * inv_freq[i] */
+} relkl_rotary_plan;
+
+/* Rotates 1..3 tensors (Q, K and V of a layer) in one launch:
+ *
+ *   (a, b) -> mscale (a cos - b sin, b cos + a sin)      (inverse = 0)
+ *   (a, b) -> mscale (a cos + b sin, b cos - a sin)      (inverse = 1)
+ *
+ * for every pair of the first rot entries; the others keep their values.
+ * Angles are formed and reduced in double precision, the rotation runs in
+ * float32 and the result is rounded once to y_dtype.  Frequencies scaled for
+ * long contexts and their factor are the caller's (inv_freq, mscale).
+ * Tensors may have any strides whose elements of y do not overlap.  y may be x
+ * itself, with the same strides and type (the rotation in place); any other
+ * overlap of an x with a y is refused, as far as their address ranges tell.
+ * inv_freq is 8-byte aligned, positions to its type.  1 <= d <= 512;
+ * B, N, H >= 0 (zero work is a no-op).  RELKL_ERR_INVALID for anything else.
+ * Any alignment that the types allow is taken; strides and bases that are
+ * multiples of 16 bytes are fastest.  Asynchronous on `stream`.              */
+relkl_status relkl_rotary(int32_t n_tensors, const relkl_rotary_tensor* tensors,
+                          const relkl_rotary_plan* plan, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
