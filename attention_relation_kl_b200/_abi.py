@@ -113,8 +113,7 @@ def _declare(lib):
     lib.relkl_weight_grad.argtypes = [ctypes.c_int64, i32, i32, _vp, _vp, _vp, _vp,
                                       ctypes.c_size_t, _vp]
     lib.relkl_rotary.restype = ctypes.c_int
-    lib.relkl_rotary.argtypes = [i32, ctypes.POINTER(relkl_rotary_tensor),
-                                 ctypes.POINTER(relkl_rotary_plan), _vp]
+    lib.relkl_rotary.argtypes = [i32, _vp, _vp, _vp]   # arrays of the structs, or their bytes
     return lib
 
 

@@ -12,8 +12,15 @@
 // angles are formed in double precision (positions reach 10^5 and more), which
 // costs far more than the rotation, so one thread keeps the cosines and sines
 // of its few pairs of one token in registers and runs over the heads of a
-// group with them; no table is read or written.  Heads are split into groups
-// only as far as it takes to fill the SMs.
+// group with them; no table is read or written.
+//
+// Measured (B200, copy bandwidth 6.56 TB/s): 32K tokens, Q, K and V of 32
+// heads of 128, bf16, tokens to heads: 273 us, 5.9 TB/s; gradients of 2 x 16K
+// tokens, 32 + 8 + 8 heads, fp32 heads to bf16 tokens: 182 us, 6.6 TB/s.  What
+// made the difference was how many rows are in flight, not how many bytes a
+// thread has: one head at a time at 8 blocks an SM (32 registers) against four
+// heads at 3 blocks: 285 and 321 us; loads past L1 against streaming ones: 273
+// and 279 us (182 and 193 us for the gradients).
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -40,7 +47,8 @@ __device__ __forceinline__ void pair_angle(double pos, double f, float m, float&
   s = fmaf(ch, lo, sh) * m;
 }
 
-// V consecutive elements as floats, in accesses of at most 16 bytes.
+// V consecutive elements as floats, in accesses of at most 16 bytes: loads
+// keep out of L1, where nothing is read twice, stores are the first to leave L2.
 template <typename T, int V>
 struct Vec {
   static constexpr int kBytes = V * static_cast<int>(sizeof(T));
@@ -50,16 +58,16 @@ struct Vec {
     if constexpr (kBytes % 16 == 0) {
 #pragma unroll
       for (int i = 0; i < kBytes / 16; ++i) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+        const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p) + i);
         w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
       }
     } else if constexpr (kBytes == 8) {
-      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+      const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
       w[0] = v.x; w[1] = v.y;
     } else if constexpr (kBytes == 4) {
-      w[0] = __ldcs(reinterpret_cast<const unsigned int*>(p));
+      w[0] = __ldcg(reinterpret_cast<const unsigned int*>(p));
     } else {
-      w[0] = __ldcs(reinterpret_cast<const unsigned short*>(p));
+      w[0] = __ldcg(reinterpret_cast<const unsigned short*>(p));
     }
   }
   __device__ __forceinline__ void store(T* p) const {
@@ -99,7 +107,7 @@ struct Vec {
 
 template <typename T, typename U, int V>
 __device__ __forceinline__ void move_heads(const T* x, U* y, int64_t xh, int64_t yh, int heads) {
-#pragma unroll 4
+#pragma unroll 1
   for (int h = 0; h < heads; ++h) {
     Vec<T, V> a;
     a.load(x + h * xh);
@@ -119,7 +127,7 @@ __device__ __forceinline__ void move_heads(const T* x, U* y, int64_t xh, int64_t
 // entries; with V = 1 one pair, entry by entry), or V entries behind the
 // rotated part.  blockIdx.y = head group.
 template <typename T, typename U, int V, bool HALVES>
-__global__ void __launch_bounds__(256) relkl_rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(256, 8) relkl_rotary_kernel(const __grid_constant__ RotaryParams p) {
   const int64_t item = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (item >= p.n_items) return;
   const int64_t tok = item / p.chunks;
@@ -171,7 +179,7 @@ __global__ void __launch_bounds__(256) relkl_rotary_kernel(const __grid_constant
   x += at;
   y += at;
   if constexpr (SPLIT) {
-#pragma unroll 4
+#pragma unroll 1
     for (int h = 0; h < heads; ++h) {
       Vec<T, V> lo, hi;
       lo.load(x + h * xh);
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(256) relkl_rotary_kernel(const __grid_constant
       o1.store(y + h * yh + far);
     }
   } else {
-#pragma unroll 4
+#pragma unroll 1
     for (int h = 0; h < heads; ++h) {
       Vec<T, V> in;
       in.load(x + h * xh);
@@ -217,15 +225,16 @@ cudaError_t launch(RotaryParams& p, int num_sms, cudaStream_t stream) {
   p.n_items = static_cast<int64_t>(p.B) * p.N * p.chunks;
   const int64_t blocks = (p.n_items + 255) / 256;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  // As many heads for one thread as leave the SMs four waves of four blocks
-  // (a thread's angles cost as much as several heads), but at most 16.
+  // As many heads for one thread as leave the SMs two waves of blocks, but at
+  // most 4: with 1, 2, 4, 8, 16 heads the 32K inputs took 493, 319, 279, 285,
+  // 289 us (angles weigh on the left, distant rows in flight on the right).
   int most = 1, all = 0;
   for (int r = 0; r < p.n; ++r) {
     most = p.t[r].H > most ? p.t[r].H : most;
     all += p.t[r].H;
   }
   int64_t hg = blocks * all / (static_cast<int64_t>(num_sms) * 16);
-  hg = hg < 1 ? 1 : (hg > 16 ? 16 : hg);
+  hg = hg < 1 ? 1 : (hg > 4 ? 4 : hg);
   while ((most + hg - 1) / hg * p.n > 65535) hg *= 2;   // the grid's y extent
   p.heads_per_group = static_cast<int>(hg);
   int groups = 0;

@@ -86,19 +86,30 @@ def _stream(device: torch.device, stream=None) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream=None):
+class _on:
     """Makes ``device`` current, and ``stream`` (a torch stream or a cudaStream_t
     handle) if one is given, so that what a call allocates for itself belongs to
-    the stream that uses it.  Yields the cudaStream_t handle."""
-    with contextlib.ExitStack() as st:
-        if torch.cuda.current_device() != device.index:
-            st.enter_context(torch.cuda.device(device))
-        if stream is not None:
+    the stream that uses it.  Enters as the cudaStream_t handle."""
+
+    def __init__(self, device: torch.device, stream=None):
+        self.device, self.stream, self.inner = device, stream, None
+
+    def __enter__(self) -> int:
+        index = self.device.index
+        if self.stream is None and torch.cuda.current_device() == index:
+            return torch.cuda.current_stream(index).cuda_stream
+        self.inner = contextlib.ExitStack()
+        self.inner.enter_context(torch.cuda.device(self.device))
+        if self.stream is not None:
+            stream = self.stream
             if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            st.enter_context(torch.cuda.stream(stream))
-        yield _stream(device)
+                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+            self.inner.enter_context(torch.cuda.stream(stream))
+        return torch.cuda.current_stream(index).cuda_stream
+
+    def __exit__(self, *exc) -> None:
+        if self.inner is not None:
+            self.inner.close()
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:

@@ -8,8 +8,8 @@ gives the token-major layout that ``relkl_weight_grad`` reads.
 """
 from __future__ import annotations
 
-import ctypes
 import math
+import struct
 from typing import List, NamedTuple, Optional, Sequence
 
 import torch
@@ -21,6 +21,9 @@ from .ops import _DTYPES, _cuda, _on
 __all__ = ["RotaryFreqs", "rotary_freqs", "relkl_rotary_qkv", "relkl_rotary", "Rotary", "rotary"]
 
 MAX_TENSORS = 3
+# the layouts of relkl_rotary_tensor and relkl_rotary_plan (include/relkl.h)
+_TENSOR = struct.Struct("@PP3q3qii")
+_PLAN = struct.Struct("@8iP2qifddP")
 
 
 class RotaryFreqs(NamedTuple):
@@ -121,26 +124,22 @@ def relkl_rotary_qkv(xs: Sequence[torch.Tensor], inv_freq: torch.Tensor, *,
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or \
             inv_freq.device != dev:
         raise ValueError("inv_freq must be a contiguous float64 vector on the inputs' device")
-    if 2 * inv_freq.numel() > d:
-        raise ValueError(f"inv_freq has {inv_freq.numel()} pairs, more than a head of {d} holds")
+    rot = 2 * inv_freq.numel()
+    if rot > d:
+        raise ValueError(f"inv_freq has {rot // 2} pairs, more than a head of {d} holds")
     for x in xs:
         if x.dim() != 4 or x.dtype != x0.dtype or x.device != dev or \
                 (x.shape[0], x.shape[2], x.shape[3]) != (B, N, d):
             raise ValueError("all tensors must share device, dtype, B, N and d")
         if x.stride(3) != 1 and d > 1:
             raise ValueError("the last dimension must be contiguous")
-    plan = _abi.relkl_rotary_plan()
-    plan.B, plan.N, plan.d, plan.rot = B, N, d, 2 * inv_freq.numel()
-    plan.x_dtype = _DTYPES[x0.dtype]
-    plan.interleaved, plan.inverse = int(bool(interleaved)), int(bool(inverse))
-    plan.mscale, plan.pos_scale, plan.pos_offset = float(mscale), float(pos_scale), float(pos_offset)
-    plan.inv_freq = inv_freq.data_ptr()
+    pos_ptr = pos_bytes = pos_b = pos_n = 0
     if positions is not None:
         positions = _check_positions(positions, B, N, dev)
-        plan.positions, plan.pos_bytes = positions.data_ptr() or None, positions.element_size()
-        plan.pos_stride[0], plan.pos_stride[1] = positions.stride()
-        if not plan.positions:
-            plan.pos_bytes = 0      # no token, nothing to read
+        pos_ptr = positions.data_ptr()
+        if pos_ptr:      # no token, nothing to read
+            pos_bytes = positions.element_size()
+            pos_b, pos_n = positions.stride()
     with _on(dev, stream) as handle:
         if out is None:
             out_dtype = x0.dtype if out_dtype is None else out_dtype
@@ -157,13 +156,13 @@ def relkl_rotary_qkv(xs: Sequence[torch.Tensor], inv_freq: torch.Tensor, *,
                         (y.stride(3) != 1 and d > 1):
                     raise ValueError(f"out must be {out_dtype} tensors of the inputs' shapes on "
                                      f"{dev} whose last dimension is contiguous")
-        plan.y_dtype = _DTYPES[out_dtype]
-        tensors = (_abi.relkl_rotary_tensor * n)()
-        for t, x, y, a in zip(tensors, xs, out, apply):
-            t.x, t.y = x.data_ptr(), y.data_ptr()
-            t.x_stride[:], t.y_stride[:] = x.stride()[:3], y.stride()[:3]
-            t.H, t.apply = x.shape[1], int(bool(a))
-        check(_abi.lib().relkl_rotary(n, tensors, ctypes.byref(plan), handle), "relkl_rotary")
+        tensors = b"".join([
+            _TENSOR.pack(x.data_ptr(), y.data_ptr(), *x.stride()[:3], *y.stride()[:3], x.shape[1],
+                         bool(a)) for x, y, a in zip(xs, out, apply)])
+        plan = _PLAN.pack(B, N, d, rot, _DTYPES[x0.dtype], _DTYPES[out_dtype], bool(interleaved),
+                          bool(inverse), pos_ptr, pos_b, pos_n, pos_bytes, mscale, pos_scale,
+                          pos_offset, inv_freq.data_ptr())
+        check(_abi.lib().relkl_rotary(n, tensors, plan, handle), "relkl_rotary")
     return out
 
 
