@@ -23,7 +23,7 @@ EXPORTS = ("relkl_workspace_bytes", "relkl_workspace_init", "relkl_fwd", "relkl_
            "relkl_path_for", "relkl_fwd_noalloc", "relkl_rope_bwd", "relkl_weight_grad",
            "relkl_cast_bf16", "relkl_bwd_kernel_for",
            "relkl_fwd_qkv_part", "relkl_bwd_qkv_part", "relkl_check_schedule",
-           "relkl_rotary")
+           "relkl_rotary", "relkl_adamw", "relkl_grad_norm", "relkl_grad_norm_bytes")
 
 
 class relkl_desc(ctypes.Structure):
@@ -55,6 +55,24 @@ class relkl_rotary_plan(ctypes.Structure):
                 ("pos_bytes", ctypes.c_int32), ("mscale", ctypes.c_float),
                 ("pos_scale", ctypes.c_double), ("pos_offset", ctypes.c_double),
                 ("inv_freq", ctypes.c_void_p)]
+
+
+class relkl_adamw_tensor(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("grad", "param", "copy", "m", "v", "m_scale", "v_scale")]
+    _fields_ += [("n", ctypes.c_int64), ("grad_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                 ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class relkl_adamw_plan(ctypes.Structure):
+    _fields_ = [("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32), ("lr", ctypes.c_double),
+                ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_void_p)]
+
+
+class relkl_norm_tensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 _vp = ctypes.c_void_p
@@ -114,6 +132,12 @@ def _declare(lib):
                                       ctypes.c_size_t, _vp]
     lib.relkl_rotary.restype = ctypes.c_int
     lib.relkl_rotary.argtypes = [i32, _vp, _vp, _vp]   # arrays of the structs, or their bytes
+    lib.relkl_adamw.restype = ctypes.c_int
+    lib.relkl_adamw.argtypes = [i32, _vp, _vp, _vp]
+    lib.relkl_grad_norm_bytes.restype = ctypes.c_size_t
+    lib.relkl_grad_norm_bytes.argtypes = [i32]
+    lib.relkl_grad_norm.restype = ctypes.c_int
+    lib.relkl_grad_norm.argtypes = [i32, _vp, ctypes.c_float, _vp, _vp, ctypes.c_size_t, _vp]
     return lib
 
 

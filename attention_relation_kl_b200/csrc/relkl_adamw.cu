@@ -1,0 +1,462 @@
+// One AdamW step over many tensors, and the norm of all their gradients:
+//
+//   g = coef * grad
+//   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+//
+// The states m and v are float32, or 8-bit: each block of 256 consecutive
+// elements holds m and r = sqrt(v) as e4m3 numbers times one float32 scale,
+// its largest magnitude / 448.  The root is held and not v because an e4m3
+// block spans 2^18: of v that would leave gradients 2^9 apart, of r it leaves
+// 2^18.  A positive r below the smallest code is held as the smallest code,
+// never as zero, so that no element's step is divided by eps alone.  p is
+// updated from the new m and v before they are rounded to codes.
+//
+// What bounds it: HBM.  Every byte is read once and written once (28 to 30 B
+// an element with float32 states and weights, 16 to 18 with 8-bit states), all
+// tensors of a call go in one launch (their table travels in the kernel's
+// parameters, so a captured graph needs no memory of its own for it), and the
+// statistics of an 8-bit block stay in the registers of its warp.
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "relkl_params.h"
+
+namespace relkl {
+
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int CHUNK32 = 4096;           // elements of one CTA, float32 states
+constexpr int CHUNK8 = 4096;            // 16 blocks of 256, 8-bit states
+constexpr int BLOCK8 = 256;
+constexpr float E4M3_MAX = 448.0f;
+constexpr float E4M3_MIN = 0.001953125f;   // 2^-9, the smallest positive code
+constexpr float TINY = 1.1754943508222875e-38f;
+
+struct Hyper {
+  float coef, b1, c1, b2, c2, eps, rbc2, step, decay;
+  bool skip;
+};
+
+// The step's scalars.  lr and the step number may live on the device, so that
+// a replayed graph takes their values at the time; the bias corrections are
+// formed in double precision in either case.
+__device__ __forceinline__ Hyper hyper(const AdamwPlan& a, float wd) {
+  Hyper h;
+  double lr = a.lr, bc1 = a.bc1, bc2 = a.bc2;
+  if (a.lr_dev) lr = *a.lr_dev;
+  if (a.step_dev) {
+    const double t = static_cast<double>(*a.step_dev);
+    bc1 = -expm1(t * a.log_b1);
+    bc2 = -expm1(t * a.log_b2);
+  }
+  h.coef = a.grad_scale ? *a.grad_scale : 1.0f;
+  h.skip = !isfinite(h.coef);
+  h.b1 = a.b1;
+  h.c1 = a.c1;
+  h.b2 = a.b2;
+  h.c2 = a.c2;
+  h.eps = a.eps;
+  h.rbc2 = static_cast<float>(1.0 / sqrt(bc2));
+  h.step = static_cast<float>(lr / bc1);
+  h.decay = static_cast<float>(1.0 - lr * wd);
+  return h;
+}
+
+__device__ __forceinline__ void update(const Hyper& h, float g, float& p, float& m, float& v,
+                                       float& root) {
+  g *= h.coef;
+  m = fmaf(h.b1, m, h.c1 * g);
+  v = fmaf(h.b2, v, h.c2 * g * g);
+  root = sqrtf(v);
+  p = fmaf(p, h.decay, -h.step * (m / fmaf(root, h.rbc2, h.eps)));
+}
+
+// --------------------------------------------------------- accesses
+template <typename T>
+__device__ __forceinline__ float load1(const T* p) {
+  if constexpr (sizeof(T) == 4) return __ldcg(p);
+  return __uint_as_float(
+      static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short*>(p))) << 16);
+}
+template <typename T>
+__device__ __forceinline__ void store1(T* p, float v) {
+  if constexpr (sizeof(T) == 4)
+    __stcs(p, v);
+  else
+    __stcs(reinterpret_cast<unsigned short*>(p), __bfloat16_as_ushort(__float2bfloat16_rn(v)));
+}
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float* v) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  } else {
+    const uint2 x = __ldcg(reinterpret_cast<const uint2*>(p));
+    v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
+    v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float* v) {
+  if constexpr (sizeof(T) == 4) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    __stcs(reinterpret_cast<uint2*>(p), make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                                   *reinterpret_cast<const uint32_t*>(&b)));
+  }
+}
+
+// --------------------------------------------------- float32 states
+template <typename G, typename P>
+__device__ void chunk32(const AdamwTensor& t, const Hyper& h, int64_t begin) {
+  const G* g = static_cast<const G*>(t.grad);
+  P* p = static_cast<P*>(t.param);
+  float *m = static_cast<float*>(t.m), *v = static_cast<float*>(t.v);
+  __nv_bfloat16* c = static_cast<__nv_bfloat16*>(t.copy);
+  const int64_t end = min(begin + CHUNK32, t.n);
+  const int64_t wide = t.wide ? begin + (end - begin) / 4 * 4 : begin;
+  float root;
+#pragma unroll 1
+  for (int64_t i = begin + 4 * threadIdx.x; i < wide; i += 4 * THREADS) {
+    float gg[4], pp[4], mm[4], vv[4];
+    load4(g + i, gg);
+    load4(p + i, pp);
+    load4(m + i, mm);
+    load4(v + i, vv);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) update(h, gg[k], pp[k], mm[k], vv[k], root);
+    store4(p + i, pp);
+    store4(m + i, mm);
+    store4(v + i, vv);
+    if (c) store4(c + i, pp);
+  }
+#pragma unroll 2
+  for (int64_t i = wide + threadIdx.x; i < end; i += THREADS) {
+    float pp = load1(p + i), mm = load1(m + i), vv = load1(v + i);
+    update(h, load1(g + i), pp, mm, vv, root);
+    store1(p + i, pp);
+    store1(m + i, mm);
+    store1(v + i, vv);
+    if (c) store1(c + i, pp);
+  }
+}
+
+// ----------------------------------------------------- 8-bit states
+__device__ __forceinline__ float decode1(uint8_t code) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
+}
+__device__ __forceinline__ void decode4(uint32_t codes, float* v) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const __half2 x(__nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(codes >> (16 * k)), __NV_E4M3));
+    const float2 f = __half22float2(x);
+    v[2 * k] = f.x;
+    v[2 * k + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint32_t encode4(const float* v) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// The largest of the warp's non-negative numbers (a NaN counts as larger than
+// infinity: its bits are), as a block's scale and the factor that encodes.
+__device__ __forceinline__ void block_scale(float most, float& scale, float& inv) {
+  most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+  scale = most / E4M3_MAX;
+  if (scale < TINY) scale = 0.0f;
+  inv = scale > 0.0f ? 1.0f / scale : 0.0f;
+}
+__device__ __forceinline__ float larger(float a, float b) {   // of magnitudes, NaN the largest
+  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b) & 0x7fffffffu));
+}
+
+// One warp, one block of 256: lane l holds elements 8l .. 8l + 7 in wide
+// accesses, or l, l + 32, ... (the last block, and tensors that are not
+// aligned for wide ones).
+template <typename G, typename P>
+__device__ void block8(const AdamwTensor& t, const Hyper& h, int64_t blk) {
+  const int lane = threadIdx.x & 31;
+  const int64_t first = blk * BLOCK8;
+  const bool wide = t.wide && first + BLOCK8 <= t.n;
+  const G* g = static_cast<const G*>(t.grad) + first;
+  P* p = static_cast<P*>(t.param) + first;
+  uint8_t *mc = static_cast<uint8_t*>(t.m) + first, *rc = static_cast<uint8_t*>(t.v) + first;
+  __nv_bfloat16* c = t.copy ? static_cast<__nv_bfloat16*>(t.copy) + first : nullptr;
+  const int left = static_cast<int>(min(t.n - first, static_cast<int64_t>(BLOCK8)));
+  float gg[8], pp[8], mm[8], rr[8];
+  const int at = 8 * lane;
+  const float ms = __ldcg(t.m_scale + blk), rs = __ldcg(t.v_scale + blk);
+  if (wide) {
+    const uint2 mq = __ldcg(reinterpret_cast<const uint2*>(mc + at));
+    const uint2 rq = __ldcg(reinterpret_cast<const uint2*>(rc + at));
+    load4(g + at, gg);
+    load4(g + at + 4, gg + 4);
+    load4(p + at, pp);
+    load4(p + at + 4, pp + 4);
+    decode4(mq.x, mm);
+    decode4(mq.y, mm + 4);
+    decode4(rq.x, rr);
+    decode4(rq.y, rr + 4);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = lane + 32 * k;
+      const bool in = i < left;
+      gg[k] = in ? load1(g + i) : 0.0f;
+      pp[k] = in ? load1(p + i) : 0.0f;
+      mm[k] = in ? decode1(__ldcg(mc + i)) : 0.0f;
+      rr[k] = in ? decode1(__ldcg(rc + i)) : 0.0f;
+    }
+  }
+  float mmost = 0.0f, rmost = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float m = mm[k] * ms, r = rr[k] * rs, v = r * r;
+    // an element behind the end is 0 whatever the scales are
+    if (!wide && lane + 32 * k >= left) m = v = 0.0f;
+    update(h, gg[k], pp[k], m, v, r);
+    mm[k] = m;
+    rr[k] = r;
+    mmost = larger(mmost, m);
+    rmost = larger(rmost, r);
+  }
+  float mscale, minv, rscale, rinv;
+  block_scale(mmost, mscale, minv);
+  block_scale(rmost, rscale, rinv);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    mm[k] *= minv;
+    const float r = rr[k] * rinv;
+    rr[k] = (rr[k] > 0.0f && rinv > 0.0f && r < E4M3_MIN) ? E4M3_MIN : r;
+  }
+  if (wide) {
+    store4(p + at, pp);
+    store4(p + at + 4, pp + 4);
+    if (c) {
+      store4(c + at, pp);
+      store4(c + at + 4, pp + 4);
+    }
+    __stcs(reinterpret_cast<uint2*>(mc + at), make_uint2(encode4(mm), encode4(mm + 4)));
+    __stcs(reinterpret_cast<uint2*>(rc + at), make_uint2(encode4(rr), encode4(rr + 4)));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = lane + 32 * k;
+      if (i < left) {
+        store1(p + i, pp[k]);
+        if (c) store1(c + i, pp[k]);
+        __stcs(mc + i, static_cast<uint8_t>(__nv_cvt_float_to_fp8(mm[k], __NV_SATFINITE, __NV_E4M3)));
+        __stcs(rc + i, static_cast<uint8_t>(__nv_cvt_float_to_fp8(rr[k], __NV_SATFINITE, __NV_E4M3)));
+      }
+    }
+  }
+  if (lane == 0) {
+    __stcs(t.m_scale + blk, mscale);
+    __stcs(t.v_scale + blk, rscale);
+  }
+}
+
+template <typename G, typename P>
+__device__ void chunk8(const AdamwTensor& t, const Hyper& h, int64_t begin) {
+  const int64_t last = (min(begin + CHUNK8, t.n) + BLOCK8 - 1) / BLOCK8;
+#pragma unroll 1
+  for (int64_t b = begin / BLOCK8 + (threadIdx.x >> 5); b < last; b += THREADS / 32)
+    block8<G, P>(t, h, b);
+}
+
+// The tensor of this CTA: the last whose first CTA is not behind it.
+template <int CAP>
+__device__ __forceinline__ int find(const int (&first)[CAP], int n, int block) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= block) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+}  // namespace
+
+template <int CAP, bool BITS8>
+__global__ void __launch_bounds__(THREADS) relkl_adamw_kernel(const __grid_constant__ AdamwParams<CAP> p) {
+  const int k = find(p.first, p.n, blockIdx.x);
+  const AdamwTensor& t = p.t[k];
+  const Hyper h = hyper(p.plan, t.weight_decay);
+  if (h.skip) return;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - p.first[k]) * (BITS8 ? CHUNK8 : CHUNK32);
+  using H = __nv_bfloat16;
+#define RELKL_CHUNK(G, P)                \
+  do {                                   \
+    if constexpr (BITS8)                 \
+      chunk8<G, P>(t, h, begin);         \
+    else                                 \
+      chunk32<G, P>(t, h, begin);        \
+  } while (0)
+  if (t.grad_bf16) {
+    if (t.param_bf16) RELKL_CHUNK(H, H); else RELKL_CHUNK(H, float);
+  } else {
+    if (t.param_bf16) RELKL_CHUNK(float, H); else RELKL_CHUNK(float, float);
+  }
+#undef RELKL_CHUNK
+}
+
+// ------------------------------------------------------- gradient norm
+// sqrt(sum of g^2) over all tensors.  Eight squares are summed in float32, the
+// rest in double precision, in an order that depends on the sizes and the
+// grid only, so the same gradients give the same bits.
+namespace {
+
+constexpr int NORM_CHUNK = 8192;
+
+template <typename G>
+__device__ double chunk_squares(const NormTensor& t, int64_t begin) {
+  const G* g = static_cast<const G*>(t.grad);
+  const int64_t end = min(begin + NORM_CHUNK, t.n);
+  const int64_t wide = t.wide ? begin + (end - begin) / 8 * 8 : begin;
+  double sum = 0.0;
+#pragma unroll 2
+  for (int64_t i = begin + 8 * threadIdx.x; i < wide; i += 8 * blockDim.x) {
+    float x[8];
+    load4(g + i, x);
+    load4(g + i + 4, x + 4);
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = fmaf(x[k], x[k], s);
+    sum += s;
+  }
+  for (int64_t i = wide + threadIdx.x; i < end; i += blockDim.x) {
+    const float x = load1(g + i);
+    sum += static_cast<double>(x) * x;
+  }
+  return sum;
+}
+
+__device__ double block_sum(double v) {
+  __shared__ double part[32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_down_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = threadIdx.x < blockDim.x / 32 ? part[threadIdx.x] : 0.0;
+  if (threadIdx.x < 32)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_down_sync(0xffffffffu, v, o);
+  return v;   // thread 0's
+}
+
+// out[0]: the norm; out[1]: what gradients are multiplied by so that their norm
+// is at most max_norm, NaN where the norm is no finite number.
+__device__ void write_norm(float* out, double squares, float max_norm) {
+  const float norm = static_cast<float>(sqrt(squares));
+  out[0] = norm;
+  const double coef = static_cast<double>(max_norm) / (static_cast<double>(norm) + 1e-6);
+  out[1] = isfinite(norm) ? static_cast<float>(coef < 1.0 ? coef : 1.0) : __int_as_float(0x7fc00000);
+}
+
+}  // namespace
+
+template <int CAP>
+__global__ void __launch_bounds__(512) relkl_grad_norm_kernel(const __grid_constant__ NormParams<CAP> p) {
+  double sum = 0.0;
+  for (int chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
+    const int k = find(p.first, p.n, chunk);
+    const int64_t begin = static_cast<int64_t>(chunk - p.first[k]) * NORM_CHUNK;
+    sum += p.t[k].bf16 ? chunk_squares<__nv_bfloat16>(p.t[k], begin)
+                       : chunk_squares<float>(p.t[k], begin);
+  }
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) {
+    if (p.out)
+      write_norm(p.out, sum, p.max_norm);
+    else
+      p.partial[blockIdx.x] = sum;
+  }
+}
+
+__global__ void __launch_bounds__(512)
+relkl_norm_finish_kernel(const double* partial, int n, float max_norm, float* out) {
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) sum += partial[i];
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) write_norm(out, sum, max_norm);
+}
+
+// ------------------------------------------------------------- launches
+namespace {
+
+template <int CAP>
+cudaError_t adamw_group(const AdamwTensor* t, int n, const AdamwPlan& plan, bool bits8,
+                        cudaStream_t stream) {
+  AdamwParams<CAP> p;
+  p.plan = plan;
+  p.n = n;
+  int64_t blocks = 0;
+  const int chunk = bits8 ? CHUNK8 : CHUNK32;
+  for (int k = 0; k < n; ++k) {
+    p.t[k] = t[k];
+    p.first[k] = static_cast<int>(blocks);
+    blocks += (t[k].n + chunk - 1) / chunk;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  }
+  if (bits8)
+    relkl_adamw_kernel<CAP, true><<<static_cast<unsigned>(blocks), THREADS, 0, stream>>>(p);
+  else
+    relkl_adamw_kernel<CAP, false><<<static_cast<unsigned>(blocks), THREADS, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int CAP>
+cudaError_t norm_group(const NormTensor* t, int n, int64_t chunks, int grid, double* partial,
+                       float* out, float max_norm, cudaStream_t stream) {
+  NormParams<CAP> p;
+  p.n = n;
+  p.chunks = static_cast<int>(chunks);
+  p.partial = partial;
+  p.out = out;
+  p.max_norm = max_norm;
+  int64_t at = 0;
+  for (int k = 0; k < n; ++k) {
+    p.t[k] = t[k];
+    p.first[k] = static_cast<int>(at);
+    at += (t[k].n + NORM_CHUNK - 1) / NORM_CHUNK;
+  }
+  relkl_grad_norm_kernel<CAP><<<grid, 512, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Tensors are those with elements, at most kAdamwMost of them.
+cudaError_t launch_adamw(const AdamwTensor* t, int n, const AdamwPlan& plan, bool bits8,
+                         cudaStream_t stream) {
+  return n <= kAdamwFew ? adamw_group<kAdamwFew>(t, n, plan, bits8, stream)
+                        : adamw_group<kAdamwMost>(t, n, plan, bits8, stream);
+}
+
+int64_t norm_chunks(int64_t n) { return (n + NORM_CHUNK - 1) / NORM_CHUNK; }
+
+// One group's sum: into `out` as a norm where one CTA does all (grid 1), else
+// `grid` partial sums.
+cudaError_t launch_grad_norm(const NormTensor* t, int n, int64_t chunks, int grid, double* partial,
+                             float* out, float max_norm, cudaStream_t stream) {
+  return n <= kAdamwFew ? norm_group<kAdamwFew>(t, n, chunks, grid, partial, out, max_norm, stream)
+                        : norm_group<kAdamwMost>(t, n, chunks, grid, partial, out, max_norm, stream);
+}
+
+cudaError_t launch_norm_finish(const double* partial, int n, float max_norm, float* out,
+                               cudaStream_t stream) {
+  relkl_norm_finish_kernel<<<1, 512, 0, stream>>>(partial, n, max_norm, out);
+  return cudaGetLastError();
+}
+
+}  // namespace relkl

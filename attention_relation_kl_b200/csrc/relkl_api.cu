@@ -2,6 +2,7 @@
 // TMA descriptor encoding, kernel selection and launch.  No allocation and no
 // state survives a call except two process-wide settings (the wait timeout
 // and a per-device SM-count cache).
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -34,6 +35,13 @@ cudaError_t launch_rope_bwd(const float* dx, void* out, int B, int H, int N, int
                             cudaStream_t stream);
 cudaError_t launch_rotary(RotaryParams& p, bool x_bf16, bool y_bf16, bool interleaved,
                           int num_sms, cudaStream_t stream);
+cudaError_t launch_adamw(const AdamwTensor* t, int n, const AdamwPlan& plan, bool bits8,
+                         cudaStream_t stream);
+int64_t norm_chunks(int64_t n);
+cudaError_t launch_grad_norm(const NormTensor* t, int n, int64_t chunks, int grid, double* partial,
+                             float* out, float max_norm, cudaStream_t stream);
+cudaError_t launch_norm_finish(const double* partial, int n, float max_norm, float* out,
+                               cudaStream_t stream);
 using EncodeTiledFnG = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                     const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                     const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -750,6 +758,174 @@ relkl_status relkl_rotary(int32_t n_tensors, const relkl_rotary_tensor* tensors,
   if ((s = device_info(&dev)) != RELKL_OK) return s;
   cudaError_t e = launch_rotary(p, a.x_dtype == RELKL_BF16, a.y_dtype == RELKL_BF16,
                                 a.interleaved != 0, dev.sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
+}
+
+relkl_status relkl_adamw(int32_t n_tensors, const relkl_adamw_tensor* tensors,
+                         const relkl_adamw_plan* plan, void* stream) {
+  NvtxRange nvtx_range("relkl_adamw");
+  if (n_tensors < 0 || !plan || (n_tensors > 0 && !tensors)) return RELKL_ERR_INVALID;
+  const relkl_adamw_plan& a = *plan;
+  if ((a.state_bits != 32 && a.state_bits != 8) || a.reserved != 0) return RELKL_ERR_INVALID;
+  auto number = [](double x) { return std::isfinite(x) && x >= 0.0; };
+  if (!(a.beta1 >= 0.0 && a.beta1 < 1.0 && a.beta2 >= 0.0 && a.beta2 < 1.0) || !number(a.eps))
+    return RELKL_ERR_INVALID;
+  if (a.lr_dev ? !aligned(a.lr_dev, 4) : !number(a.lr)) return RELKL_ERR_INVALID;
+  if (a.step_dev ? !aligned(a.step_dev, 8) : a.step < 1) return RELKL_ERR_INVALID;
+  if (!aligned(a.grad_scale, 4)) return RELKL_ERR_INVALID;
+  const bool bits8 = a.state_bits == 8;
+  for (int32_t k = 0; k < n_tensors; ++k) {
+    const relkl_adamw_tensor& t = tensors[k];
+    if (t.n < 0 || t.n > (int64_t(1) << 40) || t.reserved != 0 || !number(t.weight_decay))
+      return RELKL_ERR_INVALID;
+    if ((t.grad_dtype != RELKL_BF16 && t.grad_dtype != RELKL_FP32) ||
+        (t.param_dtype != RELKL_BF16 && t.param_dtype != RELKL_FP32))
+      return RELKL_ERR_INVALID;
+    if (t.n == 0) continue;
+    const size_t gs = t.grad_dtype == RELKL_BF16 ? 2 : 4, ps = t.param_dtype == RELKL_BF16 ? 2 : 4;
+    const size_t ss = bits8 ? 1 : 4;
+    if (!t.grad || !t.param || !t.m || !t.v || !aligned(t.grad, gs) || !aligned(t.param, ps) ||
+        !aligned(t.copy, 2) || !aligned(t.m, ss) || !aligned(t.v, ss))
+      return RELKL_ERR_INVALID;
+    if (bits8 ? (!t.m_scale || !t.v_scale || !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
+              : (t.m_scale || t.v_scale))
+      return RELKL_ERR_INVALID;
+  }
+  AdamwPlan p;
+  p.lr = a.lr;
+  p.bc1 = 1.0 - std::pow(a.beta1, static_cast<double>(a.step));
+  p.bc2 = 1.0 - std::pow(a.beta2, static_cast<double>(a.step));
+  p.log_b1 = std::log(a.beta1);
+  p.log_b2 = std::log(a.beta2);
+  p.b1 = static_cast<float>(a.beta1);
+  p.c1 = static_cast<float>(1.0 - a.beta1);
+  p.b2 = static_cast<float>(a.beta2);
+  p.c2 = static_cast<float>(1.0 - a.beta2);
+  p.eps = static_cast<float>(a.eps);
+  p.lr_dev = a.lr_dev;
+  p.step_dev = reinterpret_cast<const long long*>(a.step_dev);
+  p.grad_scale = a.grad_scale;
+  // One launch's arrays by address: a written one overlaps none.
+  struct Range { uintptr_t begin, end; bool written; };
+  auto add = [](Range* r, int& n, const void* x, int64_t bytes, bool written) {
+    if (!x) return;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(x);
+    r[n++] = Range{b, b + static_cast<uintptr_t>(bytes), written};
+  };
+  auto overlaps = [](Range* r, int n) {
+    std::sort(r, r + n, [](const Range& x, const Range& y) { return x.begin < y.begin; });
+    uintptr_t read = 0, written = 0;   // the ends so far
+    for (int i = 0; i < n; ++i) {
+      if (r[i].begin < written || (r[i].written && r[i].begin < read)) return true;
+      uintptr_t& end = r[i].written ? written : read;
+      end = r[i].end > end ? r[i].end : end;
+    }
+    return false;
+  };
+  // Twice over the call's launches: every check comes before the first launch.
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int32_t k = 0; k < n_tensors;) {
+      AdamwTensor group[kAdamwMost];
+      Range range[7 * kAdamwMost];
+      int n = 0, nr = 0;
+      for (; k < n_tensors && n < kAdamwMost; ++k) {
+        const relkl_adamw_tensor& t = tensors[k];
+        if (t.n == 0) continue;
+        const bool gb = t.grad_dtype == RELKL_BF16, pb = t.param_dtype == RELKL_BF16;
+        const int64_t blocks = (t.n + 255) / 256, ss = bits8 ? 1 : 4;
+        if (pass == 0) {
+          add(range, nr, t.grad, t.n * (gb ? 2 : 4), false);
+          add(range, nr, t.param, t.n * (pb ? 2 : 4), true);
+          add(range, nr, t.copy, t.n * 2, true);
+          add(range, nr, t.m, t.n * ss, true);
+          add(range, nr, t.v, t.n * ss, true);
+          add(range, nr, t.m_scale, blocks * 4, true);
+          add(range, nr, t.v_scale, blocks * 4, true);
+        }
+        AdamwTensor& g = group[n++];
+        g.grad = t.grad;
+        g.param = t.param;
+        g.copy = t.copy;
+        g.m = t.m;
+        g.v = t.v;
+        g.m_scale = t.m_scale;
+        g.v_scale = t.v_scale;
+        g.n = t.n;
+        g.weight_decay = t.weight_decay;
+        g.grad_bf16 = gb;
+        g.param_bf16 = pb;
+        g.wide = aligned(t.grad, gb ? 8 : 16) && aligned(t.param, pb ? 8 : 16) &&
+                 aligned(t.copy, 8) && aligned(t.m, bits8 ? 8 : 16) && aligned(t.v, bits8 ? 8 : 16);
+      }
+      if (pass == 0) {
+        if (overlaps(range, nr)) return RELKL_ERR_INVALID;
+      } else if (n > 0) {
+        cudaError_t e = launch_adamw(group, n, p, bits8, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return cuda_fail(e);
+      }
+    }
+  }
+  return RELKL_OK;
+}
+
+size_t relkl_grad_norm_bytes(int32_t n_tensors) {
+  const int64_t groups = n_tensors > 0 ? (static_cast<int64_t>(n_tensors) + kAdamwMost - 1) / kAdamwMost : 1;
+  return static_cast<size_t>(groups) * kNormGrid * sizeof(double);
+}
+
+relkl_status relkl_grad_norm(int32_t n_tensors, const relkl_norm_tensor* tensors, float max_norm,
+                             float* out, void* scratch, size_t scratch_bytes, void* stream) {
+  NvtxRange nvtx_range("relkl_grad_norm");
+  if (n_tensors < 0 || (n_tensors > 0 && !tensors) || !(max_norm > 0.0f)) return RELKL_ERR_INVALID;
+  if (!out || !aligned(out, 4)) return RELKL_ERR_INVALID;
+  if (!scratch || !aligned(scratch, 8) || scratch_bytes < relkl_grad_norm_bytes(n_tensors))
+    return RELKL_ERR_WORKSPACE;
+  int32_t used = 0;
+  int64_t all = 0;
+  for (int32_t k = 0; k < n_tensors; ++k) {
+    const relkl_norm_tensor& t = tensors[k];
+    if (t.n < 0 || t.n > (int64_t(1) << 40) || t.reserved != 0 ||
+        (t.dtype != RELKL_BF16 && t.dtype != RELKL_FP32))
+      return RELKL_ERR_INVALID;
+    if (t.n == 0) continue;
+    if (!t.grad || !aligned(t.grad, t.dtype == RELKL_BF16 ? 2 : 4)) return RELKL_ERR_INVALID;
+    ++used;
+    all += norm_chunks(t.n);
+    if (all > 0x7fffffffLL) return RELKL_ERR_UNSUPPORTED;
+  }
+  relkl_status s;
+  DevInfo dev;
+  if ((s = device_info(&dev)) != RELKL_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  double* partial = static_cast<double*>(scratch);
+  const int most = dev.sms * 4 < kNormGrid ? dev.sms * 4 : kNormGrid;
+  cudaError_t e = cudaSuccess;
+  int sums = 0;
+  for (int32_t k = 0; k < n_tensors;) {
+    NormTensor group[kAdamwMost];
+    int n = 0;
+    int64_t chunks = 0;
+    for (; k < n_tensors && n < kAdamwMost; ++k) {
+      const relkl_norm_tensor& t = tensors[k];
+      if (t.n == 0) continue;
+      NormTensor& g = group[n++];
+      g.grad = t.grad;
+      g.n = t.n;
+      g.bf16 = t.dtype == RELKL_BF16;
+      g.wide = aligned(t.grad, g.bf16 ? 8 : 16);
+      chunks += norm_chunks(t.n);
+    }
+    if (n == 0) break;
+    // a few chunks are summed and finished by one CTA in one launch
+    const bool one = all <= kNormOneCta;
+    const int grid = one ? 1 : static_cast<int>(chunks < most ? chunks : most);
+    e = launch_grad_norm(group, n, chunks, grid, partial + sums, one && used <= kAdamwMost ? out : nullptr,
+                         max_norm, st);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (one && used <= kAdamwMost) return RELKL_OK;
+    sums += grid;
+  }
+  e = launch_norm_finish(partial, sums, max_norm, out, st);
   return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
 }
 

@@ -103,4 +103,58 @@ struct RotaryParams {
   int64_t n_items;
 };
 
+// AdamW: tables of tensors travel in the kernel's parameters (32,764 bytes at
+// most); a call with few of them copies a small table.
+constexpr int kAdamwFew = 32;
+constexpr int kAdamwMost = 384;
+
+struct AdamwTensor {
+  const void* grad;
+  void *param, *copy;        // copy: bf16 or null
+  void *m, *v;               // float32, or e4m3 codes (v: of its root)
+  float *m_scale, *v_scale;  // 8-bit states: one per 256 elements
+  int64_t n;
+  float weight_decay;
+  uint8_t grad_bf16, param_bf16;
+  uint8_t wide;              // every pointer allows accesses of four (eight) elements
+};
+
+struct AdamwPlan {
+  double lr, bc1, bc2, log_b1, log_b2;
+  float b1, c1, b2, c2, eps;   // c = 1 - b
+  const float* lr_dev;         // device, or null: lr
+  const long long* step_dev;   // device, or null: bc1, bc2
+  const float* grad_scale;     // device, or null: 1
+};
+
+template <int CAP>
+struct AdamwParams {
+  AdamwPlan plan;
+  int n;
+  int first[CAP];            // a tensor's first CTA
+  AdamwTensor t[CAP];
+};
+
+constexpr int kNormGrid = 1024;     // partial sums of one launch, at most
+constexpr int kNormOneCta = 4;      // chunks that one CTA sums and finishes alone
+
+struct NormTensor {
+  const void* grad;
+  int64_t n;
+  uint8_t bf16, wide;
+};
+
+template <int CAP>
+struct NormParams {
+  int n, chunks;
+  double* partial;
+  float* out;                // null: write partial sums
+  float max_norm;
+  int first[CAP];            // a tensor's first chunk
+  NormTensor t[CAP];
+};
+
+static_assert(sizeof(AdamwParams<kAdamwMost>) <= 32764, "kernel parameters");
+static_assert(sizeof(NormParams<kAdamwMost>) <= 32764, "kernel parameters");
+
 }  // namespace relkl

@@ -1,0 +1,252 @@
+"""The update of the trained weights: AdamW over many tensors in one launch, with
+float32 or 8-bit states, and the norm of all their gradients.
+
+LinearARD trains the student's Q/K/V projections; ``relkl_weight_grad`` gives their
+gradients, and this step applies them.
+"""
+from __future__ import annotations
+
+import math
+import struct
+from itertools import repeat
+from operator import attrgetter
+from typing import List, NamedTuple, Optional, Sequence, Union
+
+import torch
+
+from . import _abi
+from ._abi import check
+from .ops import _DTYPES, _on
+
+__all__ = ["AdamWState", "adamw_state", "relkl_adamw", "relkl_grad_norm", "AdamW"]
+
+BLOCK = 256     # elements that share one scale of an 8-bit state
+_E4M3 = torch.float8_e4m3fn
+# the layouts of the structs in include/relkl.h
+_TENSOR = struct.Struct("@7Pqiifi")
+_PLAN = struct.Struct("@iiddddqPPP")
+_NORM = struct.Struct("@Pqii")
+
+_ptr, _numel, _device = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device
+_dtype, _shape = attrgetter("dtype"), attrgetter("shape")
+
+
+class AdamWState(NamedTuple):
+    """Moments of one parameter.  32 bits: ``m`` and ``v`` are float32 of the parameter's
+    shape.  8 bits: ``m`` and ``v`` are e4m3 codes of its shape (``v`` holds those of the
+    root of the second moment), with a float32 scale for each block of 256 consecutive
+    elements in ``m_scale`` and ``v_scale``."""
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+
+
+def adamw_state(param: torch.Tensor, bits: int = 32) -> AdamWState:
+    """A fresh state: zeros."""
+    if bits == 32:
+        return AdamWState(*(torch.zeros(param.shape, dtype=torch.float32, device=param.device)
+                            for _ in range(2)))
+    if bits != 8:
+        raise ValueError("states have 32 or 8 bits")
+    blocks = -(-param.numel() // BLOCK)
+    return AdamWState(*(torch.zeros(param.shape, dtype=torch.uint8, device=param.device).view(_E4M3)
+                        for _ in range(2)),
+                      *(torch.zeros(blocks, dtype=torch.float32, device=param.device)
+                        for _ in range(2)))
+
+
+def _same_device(index: int, *lists: Sequence[torch.Tensor]) -> None:
+    for ts in lists:
+        if set(map(_device, ts)) - {index}:
+            raise ValueError("all tensors must be CUDA tensors on one device (there is no CPU path)")
+        if not all(map(torch.Tensor.is_contiguous, ts)):
+            raise ValueError("tensors must be contiguous")
+
+
+def _types(ts: Sequence[torch.Tensor], what: str) -> List[int]:
+    try:
+        return [_DTYPES[t] for t in map(_dtype, ts)]
+    except KeyError as e:
+        raise TypeError(f"{what} must be bfloat16 or float32, not {e.args[0]}") from None
+
+
+def _scalar(x: torch.Tensor, dtype: torch.dtype, index: int, what: str) -> int:
+    if x.dtype != dtype or x.numel() != 1 or x.get_device() != index:
+        raise ValueError(f"{what} must be one {dtype} number on the parameters' device")
+    return x.data_ptr()
+
+
+def relkl_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
+                states: Sequence[AdamWState], *, lr: Union[float, torch.Tensor],
+                step: Union[int, torch.Tensor], betas=(0.9, 0.999), eps: float = 1e-8,
+                weight_decay: Union[float, Sequence[float]] = 0.01,
+                copies: Optional[Sequence[torch.Tensor]] = None,
+                grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One AdamW step, in place, over tensors of bf16 or float32 (parameters and
+    gradients each), contiguous and on one device.
+
+    ``step`` is the number of this step, from 1.  ``lr`` (float32) and ``step`` (int64)
+    may be CUDA tensors of one number, read when the work runs, for captured graphs.
+    ``weight_decay`` may give a number for each tensor.  ``copies`` are bf16 tensors
+    that receive the new parameters rounded.  ``grad_scale``, one float32 number on the
+    device, multiplies the gradients; where it is not finite nothing is written at all.
+    """
+    n = len(params)
+    if len(grads) != n or len(states) != n or (copies is not None and len(copies) != n):
+        raise ValueError("params, grads, states and copies need one entry for each tensor")
+    decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
+    if len(decay) != n:
+        raise ValueError("weight_decay needs one number, or one for each tensor")
+    if n == 0:
+        return
+    index = params[0].get_device()
+    if index < 0:
+        raise ValueError("params must be CUDA tensors (there is no CPU path)")
+    m, v, m_scale, v_scale = zip(*states)
+    kinds = list(map(_dtype, m))
+    if len(set(kinds)) > 1:       # one call for each kind of state
+        for kind in dict.fromkeys(kinds):
+            at = [k for k in range(n) if kinds[k] == kind]
+            pick = lambda xs: [xs[k] for k in at]  # noqa: E731
+            relkl_adamw(pick(params), pick(grads), pick(states), lr=lr, step=step, betas=betas,
+                        eps=eps, weight_decay=pick(decay),
+                        copies=None if copies is None else pick(copies), grad_scale=grad_scale,
+                        stream=stream)
+        return
+    if kinds[0] not in (torch.float32, _E4M3) or set(map(_dtype, v)) != {kinds[0]}:
+        raise TypeError("m and v must both be float32, or both float8_e4m3fn")
+    bits = 32 if kinds[0] == torch.float32 else 8
+    shapes = list(map(_shape, params))
+    for xs in (grads, m, v) if copies is None else (grads, m, v, copies):
+        if list(map(_shape, xs)) != shapes:
+            raise ValueError("a parameter's gradient, states and copy must have its shape")
+        _same_device(index, xs)
+    _same_device(index, params)
+    sizes = list(map(_numel, params))
+    if bits == 8:
+        blocks = [-(-k // BLOCK) for k in sizes]
+        for xs in (m_scale, v_scale):
+            if any(x is None for x in xs):
+                raise ValueError("8-bit states need their scales")
+            if set(map(_dtype, xs)) != {torch.float32} or list(map(_numel, xs)) != blocks:
+                raise ValueError("8-bit states need a float32 scale for each 256 elements")
+            _same_device(index, xs)
+        m_scale, v_scale = map(_ptr, m_scale), map(_ptr, v_scale)
+    else:
+        if any(x is not None for x in m_scale + v_scale):
+            raise ValueError("float32 states have no scales")
+        m_scale = v_scale = repeat(0)
+    if copies is not None and set(map(_dtype, copies)) != {torch.bfloat16}:
+        raise TypeError("copies must be bfloat16")
+    lr_ptr = step_ptr = scale_ptr = 0
+    if isinstance(lr, torch.Tensor):
+        lr, lr_ptr = 0.0, _scalar(lr, torch.float32, index, "lr")
+    if isinstance(step, torch.Tensor):
+        step, step_ptr = 1, _scalar(step, torch.int64, index, "step")
+    if grad_scale is not None:
+        scale_ptr = _scalar(grad_scale, torch.float32, index, "grad_scale")
+    table = b"".join(map(_TENSOR.pack, map(_ptr, grads), map(_ptr, params),
+                         repeat(0) if copies is None else map(_ptr, copies), map(_ptr, m),
+                         map(_ptr, v), m_scale, v_scale, sizes, _types(grads, "gradients"),
+                         _types(params, "parameters"), decay, repeat(0)))
+    plan = _PLAN.pack(bits, 0, lr, betas[0], betas[1], eps, step, lr_ptr, step_ptr, scale_ptr)
+    with _on(params[0].device, stream) as handle:
+        check(_abi.lib().relkl_adamw(n, table, plan, handle), "relkl_adamw")
+    # what autograd saved of the old values is no longer valid
+    torch.autograd.graph.increment_version(params if copies is None else [*params, *copies])
+
+
+def relkl_grad_norm(grads: Sequence[torch.Tensor], max_norm: float = math.inf, *,
+                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Two float32 numbers on the device: the norm of all gradients (bf16 or float32) taken
+    together, and the factor min(1, max_norm / (norm + 1e-6)) that clips them to
+    ``max_norm`` (NaN where the norm is not finite), for relkl_adamw's ``grad_scale``."""
+    n = len(grads)
+    if n == 0:
+        raise ValueError("no gradients")
+    index = grads[0].get_device()
+    if index < 0:
+        raise ValueError("gradients must be CUDA tensors (there is no CPU path)")
+    _same_device(index, grads)
+    device = grads[0].device
+    if out is not None and (out.dtype != torch.float32 or tuple(out.shape) != (2,) or
+                            not out.is_contiguous() or out.get_device() != index):
+        raise ValueError("out must be a contiguous float32 tensor of two numbers on the "
+                         "gradients' device")
+    lib = _abi.lib()
+    table = b"".join(map(_NORM.pack, map(_ptr, grads), map(_numel, grads),
+                         _types(grads, "gradients"), repeat(0)))
+    nbytes = lib.relkl_grad_norm_bytes(n)
+    with _on(device, stream) as handle:
+        if out is None:
+            out = torch.empty(2, dtype=torch.float32, device=device)
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        check(lib.relkl_grad_norm(n, table, max_norm, out.data_ptr(), scratch.data_ptr(), nbytes,
+                                  handle), "relkl_grad_norm")
+    return out
+
+
+class AdamW:
+    """AdamW over a fixed list of parameters, with their states and step count.
+
+    ``step(grads)`` takes the gradients in the parameters' order (None leaves a parameter as
+    it is), or the parameters' ``.grad`` without them; with ``max_norm`` the gradients are
+    clipped by the norm of all of them, and a step whose norm is not finite changes nothing
+    but the count.  The count is a host number: for a captured graph call relkl_adamw with
+    ``step`` and ``lr`` on the device.
+    """
+
+    def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas=(0.9, 0.999),
+                 eps: float = 1e-8, weight_decay: Union[float, Sequence[float]] = 0.01, *,
+                 state_bits: int = 32, max_norm: Optional[float] = None,
+                 copies: Optional[Sequence[torch.Tensor]] = None):
+        self.params = list(params)
+        self.lr, self.betas, self.eps, self.max_norm = lr, tuple(betas), eps, max_norm
+        n = len(self.params)
+        self.weight_decay = ([float(weight_decay)] * n if isinstance(weight_decay, (int, float))
+                             else list(weight_decay))
+        self.copies = None if copies is None else list(copies)
+        if len(self.weight_decay) != n or (self.copies is not None and len(self.copies) != n):
+            raise ValueError("weight_decay and copies need one entry for each parameter")
+        self.state = [adamw_state(p, state_bits) for p in self.params]
+        self.steps = 0
+
+    def step(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None) -> Optional[torch.Tensor]:
+        """Updates the parameters; returns the gradients' norm (on the device) with max_norm."""
+        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("AdamW.step counts on the host: capture relkl_adamw with step and lr "
+                               "on the device")
+        grads = [p.grad for p in self.params] if grads is None else list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError("grads need one entry for each parameter")
+        at = [k for k, g in enumerate(grads) if g is not None]
+        if not at:
+            return None
+        pick = lambda xs: [xs[k] for k in at]  # noqa: E731
+        grads = pick(grads)
+        clip = None if self.max_norm is None else relkl_grad_norm(grads, self.max_norm)
+        relkl_adamw(pick(self.params), grads, pick(self.state), lr=self.lr, step=self.steps + 1,
+                    betas=self.betas, eps=self.eps, weight_decay=pick(self.weight_decay),
+                    copies=None if self.copies is None else pick(self.copies),
+                    grad_scale=None if clip is None else clip[1:])
+        self.steps += 1
+        return None if clip is None else clip[0]
+
+    def state_dict(self) -> dict:
+        return {"steps": self.steps, "state": [tuple(s) for s in self.state]}
+
+    def load_state_dict(self, saved: dict) -> None:
+        """Copies a state_dict's values into this optimizer's states (which keep their place)."""
+        states = saved["state"]
+        if len(states) != len(self.state):
+            raise ValueError("the saved state is of another number of parameters")
+        for mine, theirs in zip(self.state, states):
+            for a, b in zip(mine, theirs):
+                if (a is None) != (b is None) or (a is not None and (a.dtype != b.dtype or a.shape != b.shape)):
+                    raise ValueError("the saved state is of other parameters or another state_bits")
+        for mine, theirs in zip(self.state, states):
+            for a, b in zip(mine, theirs):
+                if a is not None:
+                    a.copy_(b)
+        self.steps = int(saved["steps"])

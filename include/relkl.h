@@ -382,6 +382,82 @@ typedef struct {
 relkl_status relkl_rotary(int32_t n_tensors, const relkl_rotary_tensor* tensors,
                           const relkl_rotary_plan* plan, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The update of the trained weights: one AdamW step over many tensors, and the
+ * norm of all their gradients.
+ *
+ *   g = coef * grad,   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2
+ *   param = param (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+ */
+
+/* One tensor, n elements, every array contiguous and in the same order.
+ * State of 32 bits: m and v are float [n], the scales NULL.  State of 8 bits:
+ * m and v are e4m3 codes [n] (v holds those of sqrt(v)), each block of 256
+ * consecutive elements times its scale in m_scale / v_scale,
+ * float [ceil(n / 256)]: the block's largest magnitude / 448 (0 where that is
+ * below 2^-126; the block's codes are then 0).  A positive root is never held
+ * as 0 in a block that has a scale: it takes the smallest code.  A fresh state
+ * is zeros throughout, in either form.                                       */
+typedef struct {
+  const void* grad;      /* in, grad_dtype                                    */
+  void* param;           /* in and out, param_dtype                           */
+  void* copy;            /* out: bf16 copy of the new param, or NULL          */
+  void* m;               /* in and out                                        */
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;             /* 0: the tensor is passed over                      */
+  int32_t grad_dtype, param_dtype;   /* relkl_dtype                           */
+  float weight_decay;    /* finite, >= 0                                      */
+  int32_t reserved;      /* must be 0                                         */
+} relkl_adamw_tensor;
+
+typedef struct {
+  int32_t state_bits;    /* 32 or 8, for every tensor of the call             */
+  int32_t reserved;      /* must be 0                                         */
+  double lr;             /* finite, >= 0                                      */
+  double beta1, beta2;   /* in [0, 1)                                         */
+  double eps;            /* finite, >= 0                                      */
+  int64_t step;          /* t >= 1: the number of this step                   */
+  /* Values that a captured graph takes anew at each replay (DEVICE, or NULL
+   * for the ones above).  *step_dev >= 1.                                    */
+  const float* lr_dev;
+  const int64_t* step_dev;
+  /* coef (DEVICE float; NULL: 1), such as relkl_grad_norm's second number.
+   * Where it is not finite the step is left out: nothing is written.         */
+  const float* grad_scale;
+} relkl_adamw_plan;
+
+/* One step over n_tensors tensors in one launch for each 384 of them.  The new
+ * param is rounded once, from values in float32; with 8-bit states it is formed
+ * from the new m and v before these are rounded to codes.  Arrays need only the
+ * alignment of their type (16 bytes for float, 8 for the others are fastest).
+ * No array that is written may overlap another array of the call: overlaps
+ * within a launch are refused with RELKL_ERR_INVALID, as are bad numbers, null
+ * or misaligned pointers.  n_tensors = 0 is a no-op.                         */
+relkl_status relkl_adamw(int32_t n_tensors, const relkl_adamw_tensor* tensors,
+                         const relkl_adamw_plan* plan, void* stream);
+
+typedef struct {
+  const void* grad;
+  int64_t n;
+  int32_t dtype;         /* relkl_dtype                                       */
+  int32_t reserved;      /* must be 0                                         */
+} relkl_norm_tensor;
+
+/* out[0] = sqrt(sum of grad^2 over all tensors), out[1] = min(1, max_norm /
+ * (out[0] + 1e-6)), or NaN where out[0] is not finite (max_norm > 0, infinity
+ * allowed; DEVICE float [2], 4-byte aligned).  Squares are summed by eights in
+ * float32 and beyond in double precision, in an order that the sizes and the
+ * GPU fix: the same gradients give the same bits.  A gradient above 1.8e19
+ * makes the norm infinite.
+ * scratch: relkl_grad_norm_bytes(n_tensors) bytes of device memory, 8-byte
+ * aligned, used by this call's work only until it has finished.  With
+ * n_tensors = 0 the norm is 0.                                               */
+size_t relkl_grad_norm_bytes(int32_t n_tensors);
+relkl_status relkl_grad_norm(int32_t n_tensors, const relkl_norm_tensor* tensors, float max_norm,
+                             float* out, void* scratch, size_t scratch_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
