@@ -23,7 +23,8 @@ EXPORTS = ("relkl_workspace_bytes", "relkl_workspace_init", "relkl_fwd", "relkl_
            "relkl_path_for", "relkl_fwd_noalloc", "relkl_rope_bwd", "relkl_weight_grad",
            "relkl_cast_bf16", "relkl_bwd_kernel_for",
            "relkl_fwd_qkv_part", "relkl_bwd_qkv_part", "relkl_check_schedule",
-           "relkl_rotary", "relkl_adamw", "relkl_grad_norm", "relkl_grad_norm_bytes")
+           "relkl_rotary", "relkl_adamw", "relkl_grad_norm", "relkl_grad_norm_bytes",
+           "relkl_quantize_rows", "relkl_matmul_i8", "relkl_linear_i8", "relkl_linear_i8_bytes")
 
 
 class relkl_desc(ctypes.Structure):
@@ -138,6 +139,17 @@ def _declare(lib):
     lib.relkl_grad_norm_bytes.argtypes = [i32]
     lib.relkl_grad_norm.restype = ctypes.c_int
     lib.relkl_grad_norm.argtypes = [i32, _vp, ctypes.c_float, _vp, _vp, ctypes.c_size_t, _vp]
+    i64, size = ctypes.c_int64, ctypes.c_size_t
+    lib.relkl_quantize_rows.restype = ctypes.c_int
+    lib.relkl_quantize_rows.argtypes = [i64, i32, _vp, i32, i64, _vp, i64, _vp, _vp]
+    lib.relkl_matmul_i8.restype = ctypes.c_int
+    lib.relkl_matmul_i8.argtypes = [i64, i32, i32, _vp, i64, _vp, _vp, i64, _vp, _vp, _vp, i32, i64,
+                                    _vp, size, _vp]
+    lib.relkl_linear_i8_bytes.restype = size
+    lib.relkl_linear_i8_bytes.argtypes = [i64, i32]
+    lib.relkl_linear_i8.restype = ctypes.c_int
+    lib.relkl_linear_i8.argtypes = [i64, i32, i32, _vp, i32, i64, _vp, i64, _vp, _vp, _vp, i32, i64,
+                                    _vp, size, _vp, size, _vp]
     return lib
 
 

@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "librelkl.so")
 SOURCES = ["relkl_api.cu", "relkl_tc.cu", "relkl_simt.cu", "relkl_chain.cu", "relkl_gemm.cu",
-           "relkl_rotary.cu", "relkl_adamw.cu"]
+           "relkl_rotary.cu", "relkl_adamw.cu", "relkl_int8.cu"]
 HEADERS = ["relkl_device.cuh", "relkl_params.h"]
 
 NVCC_FLAGS = [

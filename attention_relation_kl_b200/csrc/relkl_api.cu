@@ -42,6 +42,9 @@ cudaError_t launch_grad_norm(const NormTensor* t, int n, int64_t chunks, int gri
                              float* out, float max_norm, cudaStream_t stream);
 cudaError_t launch_norm_finish(const double* partial, int n, float max_norm, float* out,
                                cudaStream_t stream);
+cudaError_t launch_quantize_rows(const RowsParams& p, bool x_bf16, cudaStream_t stream);
+cudaError_t launch_gemv_i8(const GemvParams& p, bool x_bf16, bool y_bf16, cudaStream_t stream);
+cudaError_t launch_gemm_i8(I8Params& p, const I8Call& c, bool y_bf16, int num_sms, cudaStream_t stream);
 using EncodeTiledFnG = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                     const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                     const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -333,6 +336,61 @@ relkl_status build_simt(int32_t n_rel, const relkl_desc* descs, const void* cons
   const int nblk32 = ((d0.cu_seqlens ? d0.max_seqlen : d0.N) + 31) / 32;
   p->nblk_local = part < nblk32 ? (nblk32 - part + n_parts - 1) / n_parts : 0;
   return RELKL_OK;
+}
+
+// ---- products in 8-bit integers
+constexpr int64_t kMostStride = int64_t(1) << 48;   // keeps every offset far below 2^63
+
+bool element_type(int32_t t) { return t == RELKL_BF16 || t == RELKL_FP32; }
+size_t element_size(int32_t t) { return t == RELKL_BF16 ? 2 : 4; }
+
+bool rows_ok(int64_t rows, int32_t K) {
+  return rows >= 0 && rows <= (int64_t(1) << 31) && K > 0 && K < 131072;
+}
+bool codes_ok(const int8_t* q, int64_t stride, int32_t K) {
+  return q && aligned(q, 16) && stride >= K && stride % 16 == 0 && stride <= (int64_t(1) << 39);
+}
+bool matrix_ok(const void* x, int32_t dtype, int64_t stride, int32_t K) {
+  return x && element_type(dtype) && aligned(x, element_size(dtype)) && stride >= K &&
+         stride <= kMostStride;
+}
+// rows of a matrix start at 16-byte boundaries
+bool wide_rows(const void* x, int32_t dtype, int64_t stride) {
+  return aligned(x, 16) && stride * static_cast<int64_t>(element_size(dtype)) % 16 == 0;
+}
+int64_t code_pitch(int32_t K) { return (static_cast<int64_t>(K) + 15) / 16 * 16; }
+bool few_rows(int64_t rows, int32_t K) {
+  return rows <= kGemvRows && rows * code_pitch(K) <= kGemvBytes;
+}
+
+relkl_status matmul_i8(int64_t rows, int32_t cols, int32_t K, const int8_t* q, int64_t q_stride,
+                       const float* q_scale, const int8_t* w, int64_t w_stride,
+                       const float* w_scale, const float* bias, void* y, int32_t y_dtype,
+                       int64_t y_stride, void* ws, const DevInfo& dev, cudaStream_t stream) {
+  if (dev.major != 10) return RELKL_ERR_UNSUPPORTED;
+  I8Call c = {q, w, q_stride, w_stride, K, encode_fn()};
+  if (!c.encode) return RELKL_ERR_CUDA;
+  I8Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.x_scale = q_scale;
+  p.w_scale = w_scale;
+  p.bias = bias;
+  p.y = y;
+  p.rows = rows;
+  p.y_stride = y_stride;
+  p.cols = cols;
+  p.y_wide = wide_rows(y, y_dtype, y_stride);
+  p.status = reinterpret_cast<DevStatus*>(ws);
+  p.timeout_ns = g_timeout_ns.load();
+  cudaError_t e = launch_gemm_i8(p, c, y_dtype == RELKL_BF16, dev.sms, stream);
+  return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
+}
+
+relkl_status quantize_rows(int64_t rows, int32_t K, const void* x, int32_t x_dtype, int64_t x_stride,
+                           int8_t* q, int64_t q_stride, float* scale, cudaStream_t stream) {
+  RowsParams p = {x, q, scale, rows, x_stride, q_stride, K, wide_rows(x, x_dtype, x_stride)};
+  cudaError_t e = launch_quantize_rows(p, x_dtype == RELKL_BF16, stream);
+  return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
 }
 
 // Index of relation r's segment (relations without units have none).
@@ -927,6 +985,74 @@ relkl_status relkl_grad_norm(int32_t n_tensors, const relkl_norm_tensor* tensors
   }
   e = launch_norm_finish(partial, sums, max_norm, out, st);
   return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
+}
+
+relkl_status relkl_quantize_rows(int64_t rows, int32_t K, const void* x, int32_t x_dtype,
+                                 int64_t x_stride, int8_t* q, int64_t q_stride, float* scale,
+                                 void* stream) {
+  NvtxRange nvtx_range("relkl_quantize_rows");
+  if (!rows_ok(rows, K)) return RELKL_ERR_INVALID;
+  if (rows == 0) return RELKL_OK;
+  if (!matrix_ok(x, x_dtype, x_stride, K) || !codes_ok(q, q_stride, K) || !scale || !aligned(scale, 4))
+    return RELKL_ERR_INVALID;
+  return quantize_rows(rows, K, x, x_dtype, x_stride, q, q_stride, scale,
+                       static_cast<cudaStream_t>(stream));
+}
+
+relkl_status relkl_matmul_i8(int64_t rows, int32_t cols, int32_t K, const int8_t* q,
+                             int64_t q_stride, const float* q_scale, const int8_t* w,
+                             int64_t w_stride, const float* w_scale, const float* bias, void* y,
+                             int32_t y_dtype, int64_t y_stride, void* ws, size_t ws_bytes,
+                             void* stream) {
+  NvtxRange nvtx_range("relkl_matmul_i8");
+  if (!rows_ok(rows, K) || cols < 0) return RELKL_ERR_INVALID;
+  if (rows == 0 || cols == 0) return RELKL_OK;
+  if (!codes_ok(q, q_stride, K) || !codes_ok(w, w_stride, K) || !matrix_ok(y, y_dtype, y_stride, cols) ||
+      !q_scale || !w_scale || !aligned(q_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4))
+    return RELKL_ERR_INVALID;
+  relkl_status s = check_ws(ws, ws_bytes);
+  if (s != RELKL_OK) return s;
+  DevInfo dev;
+  if ((s = device_info(&dev)) != RELKL_OK) return s;
+  return matmul_i8(rows, cols, K, q, q_stride, q_scale, w, w_stride, w_scale, bias, y, y_dtype,
+                   y_stride, ws, dev, static_cast<cudaStream_t>(stream));
+}
+
+size_t relkl_linear_i8_bytes(int64_t rows, int32_t K) {
+  if (!rows_ok(rows, K) || few_rows(rows, K)) return 0;
+  return static_cast<size_t>(rows * code_pitch(K) + rows * 4);
+}
+
+relkl_status relkl_linear_i8(int64_t rows, int32_t cols, int32_t K, const void* x,
+                             int32_t x_dtype, int64_t x_stride, const int8_t* w, int64_t w_stride,
+                             const float* w_scale, const float* bias, void* y, int32_t y_dtype,
+                             int64_t y_stride, void* scratch, size_t scratch_bytes, void* ws,
+                             size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("relkl_linear_i8");
+  if (!rows_ok(rows, K) || cols < 0) return RELKL_ERR_INVALID;
+  if (rows == 0 || cols == 0) return RELKL_OK;
+  if (!matrix_ok(x, x_dtype, x_stride, K) || !codes_ok(w, w_stride, K) ||
+      !matrix_ok(y, y_dtype, y_stride, cols) || !w_scale || !aligned(w_scale, 4) || !aligned(bias, 4))
+    return RELKL_ERR_INVALID;
+  relkl_status s = check_ws(ws, ws_bytes);
+  if (s != RELKL_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (few_rows(rows, K)) {
+    GemvParams p = {x, w, w_scale, bias, y, x_stride, w_stride, y_stride, static_cast<int>(rows),
+                    cols, K, wide_rows(x, x_dtype, x_stride)};
+    cudaError_t e = launch_gemv_i8(p, x_dtype == RELKL_BF16, y_dtype == RELKL_BF16, st);
+    return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
+  }
+  if (!scratch || !aligned(scratch, 16) || scratch_bytes < relkl_linear_i8_bytes(rows, K))
+    return RELKL_ERR_WORKSPACE;
+  DevInfo dev;
+  if ((s = device_info(&dev)) != RELKL_OK) return s;
+  int8_t* q = static_cast<int8_t*>(scratch);
+  const int64_t pitch = code_pitch(K);
+  float* scale = reinterpret_cast<float*>(q + rows * pitch);
+  if ((s = quantize_rows(rows, K, x, x_dtype, x_stride, q, pitch, scale, st)) != RELKL_OK) return s;
+  return matmul_i8(rows, cols, K, q, pitch, scale, w, w_stride, w_scale, bias, y, y_dtype, y_stride,
+                   ws, dev, st);
 }
 
 relkl_status relkl_cast_bf16(const float* src, void* dst, int64_t n, void* stream) {

@@ -1,0 +1,587 @@
+// Products in 8-bit integers with a scale for each token and each channel:
+//
+//   y[r, c] = sx[r] sw[c] sum_k qx[r, k] qw[c, k] + bias[c]
+//
+// with qx = rint(127 x / max|x_r|), sx = max|x_r| / 127 formed per call, and
+// the frozen teacher's weights qw [cols, K], sw [cols] laid out once.  The sum
+// is exact in int32, so neither the split of K nor any order changes a bit;
+// it becomes float32 once, is scaled, and rounded once to the output's type.
+//
+// Three kernels:
+//   * relkl_quantize_rows_kernel: one pass over the rows; HBM.
+//   * relkl_gemv_i8_kernel, up to kGemvRows rows: every CTA codes the rows for
+//     itself in shared memory (they are small and in L2) while its warps'
+//     weights are on the way, then one warp per channel sums with dp4a.  Bound
+//     by the weights' bytes, and at these sizes by the launch.
+//   * relkl_gemm_i8_kernel: tcgen05.mma kind::i8 (s8 x s8 -> s32) with both
+//     operands K-major in 128-byte swizzled shared memory, fed by TMA.
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "relkl_device.cuh"
+#include "relkl_params.h"
+
+namespace relkl {
+
+namespace {
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// The magnitude's bits order as the magnitudes do, with NaN above infinity.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// rint(127 x / most), exactly.  The float32 quotient is off by less than
+// 127 * 2^-22, so it decides unless it lies within 1e-4 of a half; there, and
+// where 127 / most leaves float32's range, the quotient is taken in double
+// precision, which tells every half from its neighbours: 254 x and an odd
+// multiple of most, both of at most 32 bits, differ by 2^-32 of themselves or
+// not at all.
+struct RowCoder {
+  float most, inv;
+  bool easy;
+  __device__ __forceinline__ explicit RowCoder(uint32_t bits) {
+    most = __uint_as_float(bits);
+    easy = most > 1e-30f && most < 1e30f;
+    inv = easy ? 127.0f / most : 0.0f;
+  }
+  __device__ __forceinline__ bool empty() const { return !(most > 0.0f) || !isfinite(most); }
+  // 0 for a row of zeros, NaN for a row that holds an infinity or a NaN: its
+  // products are NaN
+  __device__ __forceinline__ float scale() const {
+    return isfinite(most) ? most / 127.0f : __int_as_float(0x7fc00000);
+  }
+  __device__ __forceinline__ int code(float x) const {
+    const float q = x * inv;
+    const float r = rintf(q);
+    if (easy && fabsf(fabsf(q - r) - 0.5f) > 1e-4f) return static_cast<int>(r);
+    if (empty()) return 0;
+    return static_cast<int>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(most)));
+  }
+};
+
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
+  return (a & 0xff) | ((b & 0xff) << 8) | ((c & 0xff) << 16) | (static_cast<uint32_t>(d) << 24);
+}
+
+// Eight consecutive elements as floats (16 bytes of bf16, 32 of float32).
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 w = __ldcg(reinterpret_cast<const uint4*>(p));
+  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(a[i] << 16);
+    v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+
+template <typename U>
+__device__ __forceinline__ U from_float(float v) {
+  if constexpr (sizeof(U) == 4)
+    return v;
+  else
+    return __float2bfloat16_rn(v);
+}
+
+}  // namespace
+
+// ------------------------------------------------------------ row codes
+// One warp per row.  A lane keeps HOLD groups of eight elements between the
+// search for the largest and the coding; what a longer row has beyond them is
+// read again (from L2).  `wide`: rows start at 16-byte boundaries in both
+// arrays, so groups of eight can move at once.
+template <typename T>
+__global__ void __launch_bounds__(256) relkl_quantize_rows_kernel(const RowsParams p) {
+  constexpr int HOLD = 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= p.rows) return;
+  const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+  int8_t* q = p.q + row * p.q_stride;
+  const int groups = p.wide ? p.K / 8 : 0;
+  float v[HOLD][8];
+  uint32_t most = 0;
+#pragma unroll
+  for (int h = 0; h < HOLD; ++h) {
+    const int g = h * 32 + lane;
+    if (g < groups) {
+      load8(x + 8 * g, v[h]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) most = max(most, magnitude(v[h][k]));
+    }
+  }
+  for (int g = HOLD * 32 + lane; g < groups; g += 32) {
+    float w[8];
+    load8(x + 8 * g, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) most = max(most, magnitude(w[k]));
+  }
+  for (int i = 8 * groups + lane; i < p.K; i += 32) most = max(most, magnitude(to_float(x[i])));
+  const RowCoder coder(warp_max(most));
+  auto put = [&](int g, const float(&w)[8]) {
+    int c[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c[k] = coder.code(w[k]);
+    __stcg(reinterpret_cast<uint2*>(q + 8 * g),
+           make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7])));
+  };
+#pragma unroll
+  for (int h = 0; h < HOLD; ++h)
+    if (h * 32 + lane < groups) put(h * 32 + lane, v[h]);
+  for (int g = HOLD * 32 + lane; g < groups; g += 32) {
+    float w[8];
+    load8(x + 8 * g, w);
+    put(g, w);
+  }
+  for (int i = 8 * groups + lane; i < p.K; i += 32)
+    q[i] = static_cast<int8_t>(coder.code(to_float(x[i])));
+  if (lane == 0) p.scale[row] = coder.scale();
+}
+
+// ------------------------------------------------------------ few rows
+// Shared memory: the rows' codes, each padded with zeros to 16 bytes.
+template <typename T, typename U, int R>
+__global__ void __launch_bounds__(256) relkl_gemv_i8_kernel(const GemvParams p) {
+  extern __shared__ __align__(16) int8_t codes[];
+  __shared__ uint32_t part[8];
+  __shared__ float scales[R];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  const int pitch = (p.K + 15) / 16 * 16;
+  const int vecs = p.K / 16;
+  const int8_t* w = p.w + (c < p.cols ? c : 0) * p.w_stride;
+
+  // the first of the weights are on their way while the rows are coded
+  constexpr int AHEAD = 8;
+  uint4 first[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (i * 32 + lane < vecs) first[i] = __ldcg(reinterpret_cast<const uint4*>(w) + i * 32 + lane);
+
+#pragma unroll 1
+  for (int r = 0; r < R; ++r) {
+    if (r >= p.rows) break;
+    const T* x = static_cast<const T*>(p.x) + r * p.x_stride;
+    uint32_t most = 0;
+    const int groups = p.wide ? p.K / 8 : 0;
+    for (int g = threadIdx.x; g < groups; g += 256) {
+      float v[8];
+      load8(x + 8 * g, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) most = max(most, magnitude(v[k]));
+    }
+    for (int i = 8 * groups + threadIdx.x; i < p.K; i += 256)
+      most = max(most, magnitude(to_float(x[i])));
+    most = warp_max(most);
+    __syncthreads();          // the last row's maxima have been read
+    if (lane == 0) part[warp] = most;
+    __syncthreads();
+    most = part[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) most = max(most, part[k]);
+    const RowCoder coder(most);
+    int8_t* q = codes + r * pitch;
+    for (int g = threadIdx.x; g < groups; g += 256) {
+      float v[8];
+      load8(x + 8 * g, v);
+      int k[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) k[i] = coder.code(v[i]);
+      *reinterpret_cast<uint2*>(q + 8 * g) =
+          make_uint2(pack4(k[0], k[1], k[2], k[3]), pack4(k[4], k[5], k[6], k[7]));
+    }
+    for (int i = 8 * groups + threadIdx.x; i < pitch; i += 256)
+      q[i] = i < p.K ? static_cast<int8_t>(coder.code(to_float(x[i]))) : 0;
+    if (threadIdx.x == 0) scales[r] = coder.scale();
+  }
+  __syncthreads();
+  if (c >= p.cols) return;
+
+  int acc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r] = 0;
+  auto add = [&](const uint4& a, int at) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= p.rows) break;
+      const uint4 b = *reinterpret_cast<const uint4*>(codes + r * pitch + at);
+      acc[r] = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), acc[r]);
+      acc[r] = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), acc[r]);
+      acc[r] = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), acc[r]);
+      acc[r] = __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), acc[r]);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (i * 32 + lane < vecs) add(first[i], 16 * (i * 32 + lane));
+#pragma unroll 4
+  for (int i = AHEAD * 32 + lane; i < vecs; i += 32)
+    add(__ldcg(reinterpret_cast<const uint4*>(w) + i), 16 * i);
+  // the bytes behind the last whole vector, one to a lane
+  if (16 * vecs + lane < p.K) {
+    const int b = w[16 * vecs + lane];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < p.rows) acc[r] += b * codes[r * pitch + 16 * vecs + lane];
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r] = __reduce_add_sync(0xffffffffu, acc[r]);
+  if (lane == 0) {
+    const float sw = p.w_scale[c], b = p.bias ? p.bias[c] : 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < p.rows)
+        static_cast<U*>(p.y)[r * p.y_stride + c] =
+            from_float<U>(fmaf(static_cast<float>(acc[r]), scales[r] * sw, b));
+  }
+}
+
+// ------------------------------------------------------------ the product
+namespace i8 {
+
+constexpr int BM = 128, BK = 128;          // rows and K bytes of one stage
+constexpr int THREADS = 192;               // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
+constexpr unsigned long long kDrainNs = 200000000ull;
+
+template <int BN>
+struct Smem {
+  static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = BN == 256 ? 4 : 6;
+  static constexpr int BARS = STAGES * STAGE;          // full, empty, acc_full, drain
+  static constexpr int MISC = BARS + (2 * STAGES + 2) * 8;
+  static constexpr int ALLOC = MISC + 16 + 1024;
+  // a CTA's share of a split sum: 128 rows, padded against bank conflicts
+  static constexpr int PITCH = BN + 4;
+  static_assert(BM * PITCH * 4 <= BARS || BN == 256, "partial sums take the stages' place");
+  static_assert(ALLOC <= 232448, "shared memory exceeds 227 KB");
+};
+
+// s8 x s8 -> s32, dense, both operands K-major
+__host__ __device__ constexpr uint32_t idesc(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_lead(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                         uint32_t hi, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::i8 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(id), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// an address of this CTA's shared memory in the CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ int4 ld_peer(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// n consecutive sums of one row from column c0 on, scaled and stored.  Channel
+// scales and biases are the same for every lane of the warp.
+template <typename U, int N>
+__device__ __forceinline__ void store_row(const I8Params& p, int64_t row, int c0, float sx, const int (&acc)[N]) {
+  U* y = static_cast<U*>(p.y) + row * p.y_stride + c0;
+  constexpr int V = 16 / sizeof(U);
+  const int left = p.cols - c0;
+#pragma unroll
+  for (int j = 0; j < N; j += V) {
+    float v[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = min(c0 + j + k, p.cols - 1);
+      v[k] = fmaf(static_cast<float>(acc[j + k]), sx * __ldg(p.w_scale + c),
+                  p.bias ? __ldg(p.bias + c) : 0.0f);
+    }
+    if (p.y_wide && j + V <= left) {
+      if constexpr (sizeof(U) == 4)
+        __stcs(reinterpret_cast<float4*>(y + j), make_float4(v[0], v[1], v[2], v[3]));
+      else
+        __stcs(reinterpret_cast<uint4*>(y + j),
+               make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                          pack_bf16x2(v[V - 4], v[V - 3]), pack_bf16x2(v[V - 2], v[V - 1])));
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (j + k < left) y[j + k] = from_float<U>(v[k]);
+    }
+  }
+}
+
+}  // namespace i8
+
+// One output tile of 128 rows x BN channels for each cluster; its CTAs take
+// equal shares of K (cluster dimension = split) and add their sums through
+// distributed shared memory, each finishing BN / split of the columns.
+template <int BN, typename U>
+__global__ void __launch_bounds__(i8::THREADS, 1)
+relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
+  using namespace i8;
+  using S = Smem<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bars = base + S::BARS;
+  auto FULL = [&](int s) { return bars + 8u * s; };
+  auto EMPTY = [&](int s) { return bars + 8u * (S::STAGES + s); };
+  const uint32_t ACC = bars + 8u * (2 * S::STAGES), DRAIN = ACC + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + S::MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + S::MISC + 4);
+  WaitCtl wc{p.status, abort_flag, p.timeout_ns};
+
+  const int tile = blockIdx.x / p.split;
+  const int rank = blockIdx.x % p.split;
+  const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
+  const int k0 = static_cast<int>(static_cast<int64_t>(p.k_chunks) * rank / p.split);
+  const int k1 = static_cast<int>(static_cast<int64_t>(p.k_chunks) * (rank + 1) / p.split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(FULL(s), 1);
+      mbar_init(EMPTY(s), 1);
+    }
+    mbar_init(ACC, 1);
+    mbar_init(DRAIN, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), BN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t arms[S::STAGES] = {};
+      for (int kc = k0, it = 0; kc < k1; ++kc, ++it) {
+        const int s = it % S::STAGES;
+        if (!mbar_wait(EMPTY(s), ((it / S::STAGES) & 1) ^ 1, wc, W_TMA_EMPTY_J)) break;
+        const uint32_t a = base + s * S::STAGE;
+        mbar_arrive_expect_tx(FULL(s), S::STAGE);
+        tma_load_2d(a, &p.tm_a, FULL(s), kc * BK, mt * BM);
+        tma_load_2d(a + S::A_BYTES, &p.tm_b, FULL(s), kc * BK, nt * BN);
+        ++arms[s];
+      }
+      for (int s = 0; s < S::STAGES; ++s)
+        if (arms[s]) mbar_wait_drain(FULL(s), (arms[s] - 1) & 1, kDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint32_t lead = elect_leader();
+    constexpr uint32_t ID = idesc(BM, BN);
+    const uint32_t HI = sw128_desc_hi(1024);
+    const uint32_t a0 = sw128_desc_lo(base, 16), b0 = sw128_desc_lo(base + S::A_BYTES, 16);
+    bool issued = false;
+    for (int kc = k0, it = 0; kc < k1; ++kc, ++it) {
+      const int s = it % S::STAGES;
+      if (!mbar_wait_warp(FULL(s), (it / S::STAGES) & 1, wc, W_MMA_FULL_J)) break;
+      tc_fence_after();
+      const uint32_t step = s * (S::STAGE >> 4);
+#pragma unroll
+      for (int k = 0; k < BK / 32; ++k)     // 32 K bytes an instruction
+        mma_lead(lead, tmem, a0 + step + 2 * k, b0 + step + 2 * k, HI, ID, (it > 0 || k > 0) ? 1u : 0u);
+      issued = true;
+      umma_commit_lead(lead, EMPTY(s));
+      if (kc == k1 - 1) umma_commit_lead(lead, ACC);
+    }
+    if (issued) {
+      umma_commit_lead(lead, DRAIN);
+      mbar_wait_drain(DRAIN, 0, kDrainNs);
+    }
+    __syncwarp();
+  }
+  const int q = warp & 3;      // TMEM lane quarter of an epilogue warp
+  const int64_t row = static_cast<int64_t>(mt) * BM + q * 32 + lane;
+  const bool live = warp >= 2 && row < p.rows;
+  const float sx = live ? p.x_scale[row] : 0.0f;
+  if (warp >= 2) {
+    bool ok = mbar_wait(ACC, 0, wc, W_EPI_P_FULL);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      const uint32_t addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        float bits[32];
+        tmem_ld32(addr + c, bits);
+        tmem_wait_ld();
+        int acc[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[k] = __float_as_int(bits[k]);
+        if (p.split == 1) {
+          if (live && nt * BN + c < p.cols) store_row<U, 32>(p, row, nt * BN + c, sx, acc);
+        } else {
+          const uint32_t dst = base + ((q * 32 + lane) * S::PITCH + c) * 4;
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            st_shared_v4(dst + 4 * k, acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  if (p.split > 1) {
+    cluster_sync();       // every CTA's sums are in its shared memory
+    if (live) {
+      const int width = BN / p.split;     // a multiple of 8
+      const uint32_t src = base + ((q * 32 + lane) * S::PITCH + rank * width) * 4;
+#pragma unroll 1
+      for (int c = 0; c < width; c += 8) {
+        const int col = nt * BN + rank * width + c;
+        if (col >= p.cols) break;
+        int acc[8] = {};
+        for (int r = 0; r < p.split; ++r) {
+          const uint32_t from = peer(src + 4 * c, r);
+          const int4 u = ld_peer(from), v = ld_peer(from + 16);
+          acc[0] += u.x; acc[1] += u.y; acc[2] += u.z; acc[3] += u.w;
+          acc[4] += v.x; acc[5] += v.y; acc[6] += v.z; acc[7] += v.w;
+        }
+        store_row<U, 8>(p, row, col, sx, acc);
+      }
+    }
+    __syncwarp();
+    cluster_sync();       // nobody leaves while its memory is read
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, BN);
+  }
+}
+
+// ------------------------------------------------------------- launches
+cudaError_t launch_quantize_rows(const RowsParams& p, bool x_bf16, cudaStream_t stream) {
+  const int64_t blocks = (p.rows + 7) / 8;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (x_bf16)
+    relkl_quantize_rows_kernel<__nv_bfloat16><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
+  else
+    relkl_quantize_rows_kernel<float><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+namespace {
+
+template <typename T, typename U, int R>
+cudaError_t gemv(const GemvParams& p, cudaStream_t stream) {
+  const int smem = p.rows * ((p.K + 15) / 16 * 16);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(relkl_gemv_i8_kernel<T, U, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  relkl_gemv_i8_kernel<T, U, R><<<(p.cols + 7) / 8, 256, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, typename U>
+cudaError_t gemv_rows(const GemvParams& p, cudaStream_t stream) {
+  if (p.rows == 1) return gemv<T, U, 1>(p, stream);
+  if (p.rows <= 4) return gemv<T, U, 4>(p, stream);
+  return gemv<T, U, kGemvRows>(p, stream);
+}
+
+// K-major codes [rows, K] of `stride` bytes a row, as boxes of 128 bytes x `box` rows
+bool encode_codes(CUtensorMap* m, const int8_t* q, int64_t rows, int K, int64_t stride, int box,
+                  EncodeTiled encode) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+  const cuuint32_t boxes[2] = {i8::BK, static_cast<cuuint32_t>(box)}, ones[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(q), dims, strides, boxes, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, typename U>
+cudaError_t gemm(I8Params& p, const I8Call& c, cudaStream_t stream) {
+  using S = i8::Smem<BN>;
+  p.m_tiles = static_cast<int>((p.rows + i8::BM - 1) / i8::BM);
+  if (!encode_codes(&p.tm_a, c.q, p.rows, c.K, c.q_stride, i8::BM, c.encode) ||
+      !encode_codes(&p.tm_b, c.w, p.cols, c.K, c.w_stride, BN, c.encode))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * ((p.cols + BN - 1) / BN);
+  if (tiles * p.split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  auto* kernel = relkl_gemm_i8_kernel<BN, U>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::ALLOC);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
+  cfg.blockDim = dim3(i8::THREADS);
+  cfg.dynamicSmemBytes = S::ALLOC;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename U>
+cudaError_t gemm_pick(I8Params& p, const I8Call& c, int num_sms, cudaStream_t stream) {
+  const int64_t m = (p.rows + i8::BM - 1) / i8::BM;
+  p.k_chunks = (c.K + i8::BK - 1) / i8::BK;
+  auto tiles = [&](int bn) { return m * ((p.cols + bn - 1) / bn); };
+  // the widest tile that still gives every SM one; below that, narrow tiles
+  // and shares of K of at least four chunks
+  p.split = 1;
+  if (tiles(256) >= num_sms) return gemm<256, U>(p, c, stream);
+  if (tiles(128) >= num_sms) return gemm<128, U>(p, c, stream);
+  while (p.split < 8 && tiles(64) * p.split * 2 <= num_sms && p.k_chunks >= p.split * 8) p.split *= 2;
+  return gemm<64, U>(p, c, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_gemv_i8(const GemvParams& p, bool x_bf16, bool y_bf16, cudaStream_t stream) {
+  using H = __nv_bfloat16;
+  if (x_bf16) return y_bf16 ? gemv_rows<H, H>(p, stream) : gemv_rows<H, float>(p, stream);
+  return y_bf16 ? gemv_rows<float, H>(p, stream) : gemv_rows<float, float>(p, stream);
+}
+
+cudaError_t launch_gemm_i8(I8Params& p, const I8Call& c, bool y_bf16, int num_sms, cudaStream_t stream) {
+  return y_bf16 ? gemm_pick<__nv_bfloat16>(p, c, num_sms, stream) : gemm_pick<float>(p, c, num_sms, stream);
+}
+
+}  // namespace relkl

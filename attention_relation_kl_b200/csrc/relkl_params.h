@@ -154,6 +154,54 @@ struct NormParams {
   NormTensor t[CAP];
 };
 
+// Products in 8-bit integers: row codes, few rows, and the tensor-core product.
+constexpr int kGemvRows = 8;          // most rows of the kernel for few rows
+constexpr int kGemvBytes = 96 * 1024; // most bytes of their codes in shared memory
+
+struct RowsParams {
+  const void* x;
+  int8_t* q;
+  float* scale;
+  int64_t rows, x_stride, q_stride;   // strides in elements
+  int K;
+  int wide;
+};
+
+struct GemvParams {
+  const void* x;
+  const int8_t* w;
+  const float *w_scale, *bias;        // bias may be null
+  void* y;
+  int64_t x_stride, w_stride, y_stride;
+  int rows, cols, K;
+  int wide;                           // rows of x start at 16-byte boundaries
+};
+
+struct I8Params {
+  CUtensorMap tm_a;                   // codes [rows, K]: box 128 bytes x 128 rows, 128B swizzle
+  CUtensorMap tm_b;                   // weights [cols, K]: box 128 bytes x BN rows
+  const float *x_scale, *w_scale, *bias;
+  void* y;
+  int64_t rows, y_stride;
+  int cols;
+  int y_wide;                         // rows of y start at 16-byte boundaries
+  int m_tiles, k_chunks, split;       // set by the launch
+  DevStatus* status;
+  unsigned long long timeout_ns;
+};
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+struct I8Call {
+  const int8_t *q, *w;
+  int64_t q_stride, w_stride;
+  int K;
+  EncodeTiled encode;
+};
+
 static_assert(sizeof(AdamwParams<kAdamwMost>) <= 32764, "kernel parameters");
 static_assert(sizeof(NormParams<kAdamwMost>) <= 32764, "kernel parameters");
 

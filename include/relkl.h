@@ -458,6 +458,49 @@ size_t relkl_grad_norm_bytes(int32_t n_tensors);
 relkl_status relkl_grad_norm(int32_t n_tensors, const relkl_norm_tensor* tensors, float max_norm,
                              float* out, void* scratch, size_t scratch_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Products in 8-bit integers with a scale for each token and each channel, for
+ * the frozen teacher's projections, whose weights are coded once:
+ *
+ *   y[r, c] = q_scale[r] w_scale[c] sum_k q[r, k] w[c, k] + bias[c]
+ *
+ * The sum is exact in int32 (0 < K < 131072); it is rounded to float32, scaled,
+ * and rounded once to y's type.  Code arrays (q, w) are int8 row-major with a
+ * row stride in bytes that is a multiple of 16 and at least K, at 16-byte
+ * aligned addresses; what lies between K and the stride is not read.  x and y
+ * are row-major with any stride of at least K (cols) elements, at addresses
+ * aligned to their type.  rows, cols >= 0; with rows or cols 0 a call is a
+ * no-op.  q_scale, w_scale and bias are float, 4-byte aligned; bias may be
+ * NULL.  No output may overlap an input (unchecked for rows of strided views).
+ */
+
+/* Codes of the rows of x: q[r, k] = rint(127 x[r, k] / m_r), ties to even, and
+ * scale[r] = m_r / 127, with m_r the largest |x[r, k]|.  A row of zeros gets
+ * zeros and scale 0; a row that holds an infinity or a NaN gets zeros and a NaN
+ * scale.  For weights [cols, K] the rows are the channels.                   */
+relkl_status relkl_quantize_rows(int64_t rows, int32_t K, const void* x, int32_t x_dtype,
+                                 int64_t x_stride, int8_t* q, int64_t q_stride, float* scale,
+                                 void* stream);
+
+/* The product of codes (tensor cores).  ws: the workspace record of the other
+ * calls (bounded waits).                                                     */
+relkl_status relkl_matmul_i8(int64_t rows, int32_t cols, int32_t K, const int8_t* q,
+                             int64_t q_stride, const float* q_scale, const int8_t* w,
+                             int64_t w_stride, const float* w_scale, const float* bias, void* y,
+                             int32_t y_dtype, int64_t y_stride, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* relkl_quantize_rows of x and the product with its codes.  Up to 8 rows (of at
+ * most 98,304 bytes of codes together) take one kernel for both; more are coded
+ * into scratch first: relkl_linear_i8_bytes(rows, K) bytes of device memory
+ * (0 for few rows), 16-byte aligned, used by this call's work only.          */
+size_t relkl_linear_i8_bytes(int64_t rows, int32_t K);
+relkl_status relkl_linear_i8(int64_t rows, int32_t cols, int32_t K, const void* x,
+                             int32_t x_dtype, int64_t x_stride, const int8_t* w, int64_t w_stride,
+                             const float* w_scale, const float* bias, void* y, int32_t y_dtype,
+                             int64_t y_stride, void* scratch, size_t scratch_bytes, void* ws,
+                             size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
