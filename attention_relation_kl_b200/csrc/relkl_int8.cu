@@ -252,18 +252,21 @@ namespace i8 {
 constexpr int BM = 128, BK = 128;          // rows and K bytes of one stage
 constexpr int THREADS = 192;               // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
 constexpr unsigned long long kDrainNs = 200000000ull;
+constexpr int TURN_PITCH = 33;             // words of a turned row, against bank conflicts
+constexpr int TURN_BYTES = 32 * TURN_PITCH * 4;
 
 template <int BN>
 struct Smem {
   static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 256 ? 4 : 6;
-  static constexpr int BARS = STAGES * STAGE;          // full, empty, acc_full, drain
+  static constexpr int STAGES = 6;
+  static constexpr int TURN = STAGES * STAGE;          // epilogue warps' blocks
+  static constexpr int BARS = TURN + 4 * TURN_BYTES;   // full, empty, acc_full, drain
   static constexpr int MISC = BARS + (2 * STAGES + 2) * 8;
   static constexpr int ALLOC = MISC + 16 + 1024;
   // a CTA's share of a split sum: 128 rows, padded against bank conflicts
   static constexpr int PITCH = BN + 4;
-  static_assert(BM * PITCH * 4 <= BARS || BN == 256, "partial sums take the stages' place");
+  static_assert(BM * PITCH * 4 <= TURN, "partial sums take the stages' place");
   static_assert(ALLOC <= 232448, "shared memory exceeds 227 KB");
 };
 
@@ -310,33 +313,66 @@ __device__ __forceinline__ int4 ld_peer(uint32_t addr) {
   return v;
 }
 
-// n consecutive sums of one row from column c0 on, scaled and stored.  Channel
-// scales and biases are the same for every lane of the warp.
-template <typename U, int N>
-__device__ __forceinline__ void store_row(const I8Params& p, int64_t row, int c0, float sx, const int (&acc)[N]) {
+// Eight consecutive sums of one row from column c0 on, scaled and stored.
+template <typename U>
+__device__ __forceinline__ void store_eight(const I8Params& p, int64_t row, int c0, float sx, const int (&acc)[8]) {
   U* y = static_cast<U*>(p.y) + row * p.y_stride + c0;
-  constexpr int V = 16 / sizeof(U);
   const int left = p.cols - c0;
+  float v[8];
 #pragma unroll
-  for (int j = 0; j < N; j += V) {
-    float v[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int c = min(c0 + j + k, p.cols - 1);
-      v[k] = fmaf(static_cast<float>(acc[j + k]), sx * __ldg(p.w_scale + c),
-                  p.bias ? __ldg(p.bias + c) : 0.0f);
-    }
-    if (p.y_wide && j + V <= left) {
-      if constexpr (sizeof(U) == 4)
-        __stcs(reinterpret_cast<float4*>(y + j), make_float4(v[0], v[1], v[2], v[3]));
-      else
-        __stcs(reinterpret_cast<uint4*>(y + j),
-               make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                          pack_bf16x2(v[V - 4], v[V - 3]), pack_bf16x2(v[V - 2], v[V - 1])));
+  for (int k = 0; k < 8; ++k) {
+    const int c = min(c0 + k, p.cols - 1);
+    v[k] = fmaf(static_cast<float>(acc[k]), sx * __ldg(p.w_scale + c), p.bias ? __ldg(p.bias + c) : 0.0f);
+  }
+  if (p.y_wide && left >= 8) {
+    if constexpr (sizeof(U) == 4) {
+      __stcs(reinterpret_cast<float4*>(y), make_float4(v[0], v[1], v[2], v[3]));
+      __stcs(reinterpret_cast<float4*>(y) + 1, make_float4(v[4], v[5], v[6], v[7]));
     } else {
+      __stcs(reinterpret_cast<uint4*>(y), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                     pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+    }
+  } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k)
-        if (j + k < left) y[j + k] = from_float<U>(v[k]);
+    for (int k = 0; k < 8; ++k)
+      if (k < left) y[k] = from_float<U>(v[k]);
+  }
+}
+
+// A warp's 32 rows x 32 columns, one row to a lane, are turned through its
+// part of shared memory so that stores run along rows: eight columns to a lane
+// and four lanes to a row where rows of y start at 16-byte boundaries, else one
+// column to a lane.  row0, c0: the first row and column; sx: lane l's row's
+// scale.
+template <typename U>
+__device__ __forceinline__ void store_block(const I8Params& p, int* turn, int64_t row0, int c0, float sx,
+                                            const float (&bits)[32]) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();                                      // the last block has been read
+#pragma unroll
+  for (int k = 0; k < 32; ++k) turn[lane * TURN_PITCH + k] = __float_as_int(bits[k]);
+  __syncwarp();
+  if (p.y_wide) {
+    const int c = c0 + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (lane >> 2) + 8 * i;
+      const float s = __shfl_sync(0xffffffffu, sx, r);
+      int acc[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = turn[r * TURN_PITCH + (lane & 3) * 8 + k];
+      if (row0 + r < p.rows && c < p.cols) store_eight<U>(p, row0 + r, c, s, acc);
+    }
+  } else {
+    const int c = c0 + lane;
+    const bool in = c < p.cols;
+    const float sw = in ? __ldg(p.w_scale + c) : 0.0f, b = in && p.bias ? __ldg(p.bias + c) : 0.0f;
+    U* y = static_cast<U*>(p.y) + c;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      const float s = __shfl_sync(0xffffffffu, sx, r);
+      const float v = fmaf(static_cast<float>(turn[r * TURN_PITCH + lane]), s * sw, b);
+      if (in && row0 + r < p.rows) y[(row0 + r) * p.y_stride] = from_float<U>(v);
     }
   }
 }
@@ -433,6 +469,7 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
   const int64_t row = static_cast<int64_t>(mt) * BM + q * 32 + lane;
   const bool live = warp >= 2 && row < p.rows;
   const float sx = live ? p.x_scale[row] : 0.0f;
+  int* turn = reinterpret_cast<int*>(gbase + S::TURN + (warp & 3) * TURN_BYTES);
   if (warp >= 2) {
     bool ok = mbar_wait(ACC, 0, wc, W_EPI_P_FULL);
     ok = __all_sync(0xffffffffu, ok);
@@ -444,16 +481,14 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
         float bits[32];
         tmem_ld32(addr + c, bits);
         tmem_wait_ld();
-        int acc[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) acc[k] = __float_as_int(bits[k]);
         if (p.split == 1) {
-          if (live && nt * BN + c < p.cols) store_row<U, 32>(p, row, nt * BN + c, sx, acc);
+          if (nt * BN + c < p.cols) store_block<U>(p, turn, row - lane, nt * BN + c, sx, bits);
         } else {
           const uint32_t dst = base + ((q * 32 + lane) * S::PITCH + c) * 4;
 #pragma unroll
           for (int k = 0; k < 32; k += 4)
-            st_shared_v4(dst + 4 * k, acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+            st_shared_v4(dst + 4 * k, __float_as_uint(bits[k]), __float_as_uint(bits[k + 1]),
+                         __float_as_uint(bits[k + 2]), __float_as_uint(bits[k + 3]));
         }
       }
       tc_fence_before();
@@ -475,7 +510,7 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
           acc[0] += u.x; acc[1] += u.y; acc[2] += u.z; acc[3] += u.w;
           acc[4] += v.x; acc[5] += v.y; acc[6] += v.z; acc[7] += v.w;
         }
-        store_row<U, 8>(p, row, col, sx, acc);
+        store_eight<U>(p, row, col, sx, acc);
       }
     }
     __syncwarp();
@@ -486,6 +521,264 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, BN);
+  }
+}
+
+// ------------------------------------------------- the product, CTA pairs
+// A pair of CTAs (cta_group::2) computes 256 rows x BN channels: each holds its
+// 128 rows of q and half of the channels' codes, so an SM reads (128 + BN / 2)
+// x 32 bytes of shared memory for an instruction where one CTA by itself reads
+// (128 + BN) x 32; at the int8 rate the latter needs more than the 128 bytes a
+// clock that an SM has.  Persistent; the sums of one tile are read from TMEM
+// while the next one's are formed.
+namespace i8 {
+
+template <int BN>
+struct PairSmem {
+  static constexpr int A_BYTES = BM * BK, B_BYTES = BN / 2 * BK;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int TURN = STAGES * STAGE;
+  static constexpr int BARS = TURN + 4 * TURN_BYTES;   // full, empty, acc_full[2], acc_empty[2], drain
+  static constexpr int MISC = BARS + (2 * STAGES + 5) * 8;
+  static constexpr int ALLOC = MISC + 16 + 1024;
+  static_assert(ALLOC <= 232448, "shared memory exceeds 227 KB");
+};
+
+// a load into this CTA's shared memory that signals the barrier `bar` of the
+// pair's first CTA
+__device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                         uint32_t hi, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::i8 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(id), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// arrives at `bar` of both CTAs when the MMAs issued so far are done
+__device__ __forceinline__ void commit_pair(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b16 both;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "mov.b16 both, 3;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], both;\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+// arrives at `bar` of this CTA when the MMAs issued so far are done
+__device__ __forceinline__ void commit_own(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_peer(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// mbar_wait_warp for arrivals from the other CTA
+__device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity, const WaitCtl& c,
+                                                  unsigned int where) {
+  auto done = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  bool ok = done();
+  const unsigned long long t0 = globaltimer_ns();
+  while (!ok) {
+#pragma unroll 1
+    for (int i = 0; i < 16 && !ok; ++i) ok = done();
+    if (ok || *c.abort_flag) break;
+    if (globaltimer_ns() - t0 > c.timeout_ns) {
+      record_timeout(c, where);
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Tiles in bands of kBand rows of tiles, each band along all channels: the
+// pairs that run together share a few rows' and a few channels' codes, which
+// stay in L2 while the band lasts.
+constexpr int kBand = 8;
+__device__ __forceinline__ void pair_unit(const I8Params& p, int unit, int& mt, int& nt) {
+  const int band = unit / (kBand * p.n_tiles), first = band * kBand;
+  const int in = unit - band * kBand * p.n_tiles, high = min(kBand, p.m_tiles - first);
+  mt = first + in % high;
+  nt = in / high;
+}
+
+}  // namespace i8
+
+template <int BN, typename U>
+__global__ void __launch_bounds__(i8::THREADS, 1)
+relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
+  using namespace i8;
+  using S = PairSmem<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;   // the same in both CTAs
+  uint8_t* gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const uint32_t bars = base + S::BARS;
+  auto FULL = [&](int s) { return bars + 8u * s; };                       // the first CTA's are used
+  auto EMPTY = [&](int s) { return bars + 8u * (S::STAGES + s); };        // each CTA's own
+  auto ACC_FULL = [&](int b) { return bars + 8u * (2 * S::STAGES + b); };  // each CTA's own
+  auto ACC_EMPTY = [&](int b) { return bars + 8u * (2 * S::STAGES + 2 + b); };   // the first CTA's
+  const uint32_t DRAIN = bars + 8u * (2 * S::STAGES + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + S::MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + S::MISC + 4);
+  WaitCtl wc{p.status, abort_flag, p.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(FULL(s), 1);
+      mbar_init(EMPTY(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(ACC_FULL(b), 1);
+      mbar_init(ACC_EMPTY(b), 8);      // the epilogue warps of both CTAs
+    }
+    mbar_init(DRAIN, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(2 * BN)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();       // both CTAs' barriers are there
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&p.tm_a);
+      tma_prefetch_desc(&p.tm_b);
+      uint32_t it = 0;
+      uint32_t arms[S::STAGES] = {};
+      bool ok = true;
+      for (int unit = first; ok && unit < p.n_units; unit += stride) {
+        int mt, nt;
+        pair_unit(p, unit, mt, nt);
+        const int row = mt * 2 * BM + static_cast<int>(rank) * BM;
+        const int col = nt * BN + static_cast<int>(rank) * (BN / 2);
+        for (int kc = 0; kc < p.k_chunks; ++kc, ++it) {
+          const int s = it % S::STAGES;
+          if (!(ok = mbar_wait(EMPTY(s), ((it / S::STAGES) & 1) ^ 1, wc, W_TMA_EMPTY_J))) break;
+          const uint32_t a = base + s * S::STAGE;
+          const uint32_t full = peer(FULL(s), 0);
+          if (rank == 0) mbar_arrive_expect_tx(FULL(s), 2 * S::STAGE);   // both CTAs' bytes
+          ++arms[s];
+          load_pair(a, &p.tm_a, full, kc * BK, row);
+          load_pair(a + S::A_BYTES, &p.tm_b, full, kc * BK, col);
+        }
+      }
+      // the copies of both CTAs, and the first CTA's arrivals at these
+      // barriers, before either leaves
+      for (int s = 0; s < S::STAGES; ++s) {
+        if (arms[s] == 0) continue;
+        if (rank == 0) mbar_wait_drain(FULL(s), (arms[s] - 1) & 1, kDrainNs);
+        mbar_wait_drain(EMPTY(s), (arms[s] - 1) & 1, kDrainNs);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t lead = elect_leader();
+      constexpr uint32_t ID = idesc(2 * BM, BN);
+      const uint32_t HI = sw128_desc_hi(1024);
+      const uint32_t a0 = sw128_desc_lo(base, 16), b0 = sw128_desc_lo(base + S::A_BYTES, 16);
+      uint32_t it = 0, nacc = 0;
+      bool ok = true, issued = false;
+      for (int unit = first; ok && unit < p.n_units; unit += stride, ++nacc) {
+        const int ab = nacc & 1;
+        if (!(ok = wait_warp_cluster(ACC_EMPTY(ab), ((nacc >> 1) & 1) ^ 1, wc, W_MMA_P_EMPTY))) break;
+        tc_fence_after();
+        for (int kc = 0; kc < p.k_chunks; ++kc, ++it) {
+          const int s = it % S::STAGES;
+          if (!(ok = mbar_wait_warp(FULL(s), (it / S::STAGES) & 1, wc, W_MMA_FULL_J))) break;
+          tc_fence_after();
+          const uint32_t step = s * (S::STAGE >> 4);
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)
+            mma_pair(lead, tmem + ab * BN, a0 + step + 2 * k, b0 + step + 2 * k, HI, ID,
+                     (kc > 0 || k > 0) ? 1u : 0u);
+          issued = true;
+          commit_pair(lead, EMPTY(s));
+        }
+        if (!ok) break;
+        commit_pair(lead, ACC_FULL(ab));
+      }
+      if (issued) {
+        commit_own(lead, DRAIN);
+        mbar_wait_drain(DRAIN, 0, kDrainNs);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    int* turn = reinterpret_cast<int*>(gbase + S::TURN + q * TURN_BYTES);
+    const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
+    uint32_t nacc = 0;
+    for (int unit = first; unit < p.n_units; unit += stride, ++nacc) {
+      int mt, nt;
+      pair_unit(p, unit, mt, nt);
+      const int ab = nacc & 1;
+      const int64_t row0 = static_cast<int64_t>(mt) * 2 * BM + rank * BM + q * 32;
+      const float sx = row0 + lane < p.rows ? p.x_scale[row0 + lane] : 0.0f;
+      if (!mbar_wait_warp(ACC_FULL(ab), (nacc >> 1) & 1, wc, W_EPI_P_FULL)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        float bits[32];
+        tmem_ld32(tmem + lane_addr + ab * BN + c, bits);
+        tmem_wait_ld();
+        if (c == BN - 32) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_peer(peer(ACC_EMPTY(ab), 0));
+        }
+        if (nt * BN + c < p.cols) store_block<U>(p, turn, row0, nt * BN + c, sx, bits);
+      }
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();       // no copy, product or arrival is under way in the pair
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN)
+                 : "memory");
   }
 }
 
@@ -531,6 +824,24 @@ bool encode_codes(CUtensorMap* m, const int8_t* q, int64_t rows, int K, int64_t 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <typename K>
+cudaError_t launch_cluster(K kernel, const I8Params& p, unsigned grid, int cluster, int smem,
+                           cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(i8::THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <int BN, typename U>
 cudaError_t gemm(I8Params& p, const I8Call& c, cudaStream_t stream) {
   using S = i8::Smem<BN>;
@@ -543,19 +854,25 @@ cudaError_t gemm(I8Params& p, const I8Call& c, cudaStream_t stream) {
   auto* kernel = relkl_gemm_i8_kernel<BN, U>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::ALLOC);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
-  cfg.blockDim = dim3(i8::THREADS);
-  cfg.dynamicSmemBytes = S::ALLOC;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return launch_cluster(kernel, p, static_cast<unsigned>(tiles * p.split), p.split, S::ALLOC, stream);
+}
+
+template <int BN, typename U>
+cudaError_t gemm_pair(I8Params& p, const I8Call& c, int num_sms, cudaStream_t stream) {
+  using S = i8::PairSmem<BN>;
+  const int64_t m = (p.rows + 2 * i8::BM - 1) / (2 * i8::BM), n = (p.cols + BN - 1) / BN;
+  if (!encode_codes(&p.tm_a, c.q, p.rows, c.K, c.q_stride, i8::BM, c.encode) ||
+      !encode_codes(&p.tm_b, c.w, p.cols, c.K, c.w_stride, BN / 2, c.encode))
+    return cudaErrorInvalidValue;
+  if (m * n + num_sms > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  p.m_tiles = static_cast<int>(m);
+  p.n_tiles = static_cast<int>(n);
+  p.n_units = static_cast<int>(m * n);
+  auto* kernel = relkl_gemm_i8_pair_kernel<BN, U>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::ALLOC);
+  if (e != cudaSuccess) return e;
+  const int pairs = p.n_units < num_sms / 2 ? p.n_units : num_sms / 2;
+  return launch_cluster(kernel, p, 2 * pairs, 2, S::ALLOC, stream);
 }
 
 template <typename U>
@@ -563,10 +880,8 @@ cudaError_t gemm_pick(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
   const int64_t m = (p.rows + i8::BM - 1) / i8::BM;
   p.k_chunks = (c.K + i8::BK - 1) / i8::BK;
   auto tiles = [&](int bn) { return m * ((p.cols + bn - 1) / bn); };
-  // the widest tile that still gives every SM one; below that, narrow tiles
-  // and shares of K of at least four chunks
   p.split = 1;
-  if (tiles(256) >= num_sms) return gemm<256, U>(p, c, stream);
+  if (tiles(256) >= num_sms) return gemm_pair<256, U>(p, c, num_sms, stream);
   if (tiles(128) >= num_sms) return gemm<128, U>(p, c, stream);
   while (p.split < 8 && tiles(64) * p.split * 2 <= num_sms && p.k_chunks >= p.split * 8) p.split *= 2;
   return gemm<64, U>(p, c, stream);

@@ -185,7 +185,7 @@ struct I8Params {
   int64_t rows, y_stride;
   int cols;
   int y_wide;                         // rows of y start at 16-byte boundaries
-  int m_tiles, k_chunks, split;       // set by the launch
+  int m_tiles, n_tiles, n_units, k_chunks, split;   // set by the launch
   DevStatus* status;
   unsigned long long timeout_ns;
 };
