@@ -354,9 +354,9 @@ bool matrix_ok(const void* x, int32_t dtype, int64_t stride, int32_t K) {
   return x && element_type(dtype) && aligned(x, element_size(dtype)) && stride >= K &&
          stride <= kMostStride;
 }
-// rows of a matrix start at 16-byte boundaries
-bool wide_rows(const void* x, int32_t dtype, int64_t stride) {
-  return aligned(x, 16) && stride * static_cast<int64_t>(element_size(dtype)) % 16 == 0;
+// rows of a matrix start at boundaries of 16 (or so many) bytes
+bool wide_rows(const void* x, int32_t dtype, int64_t stride, int bytes = 16) {
+  return aligned(x, bytes) && stride * static_cast<int64_t>(element_size(dtype)) % bytes == 0;
 }
 int64_t code_pitch(int32_t K) { return (static_cast<int64_t>(K) + 15) / 16 * 16; }
 bool few_rows(int64_t rows, int32_t K) {
@@ -379,7 +379,7 @@ relkl_status matmul_i8(int64_t rows, int32_t cols, int32_t K, const int8_t* q, i
   p.rows = rows;
   p.y_stride = y_stride;
   p.cols = cols;
-  p.y_wide = wide_rows(y, y_dtype, y_stride);
+  p.y_wide = wide_rows(y, y_dtype, y_stride, 32) ? 2 : wide_rows(y, y_dtype, y_stride);
   p.status = reinterpret_cast<DevStatus*>(ws);
   p.timeout_ns = g_timeout_ns.load();
   cudaError_t e = launch_gemm_i8(p, c, y_dtype == RELKL_BF16, dev.sms, stream);

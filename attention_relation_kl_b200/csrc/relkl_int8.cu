@@ -34,12 +34,13 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162f
 // The magnitude's bits order as the magnitudes do, with NaN above infinity.
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// rint(127 x / most), exactly.  The float32 quotient is off by less than
-// 127 * 2^-22, so it decides unless it lies within 1e-4 of a half; there, and
-// where 127 / most leaves float32's range, the quotient is taken in double
-// precision, which tells every half from its neighbours: 254 x and an odd
-// multiple of most, both of at most 32 bits, differ by 2^-32 of themselves or
-// not at all.
+// rint(127 x / most), exactly.  The float32 product x (127 / most) is off by
+// less than 127 * 2^-22, so its nearest integer is the code unless it lies
+// within 1e-4 of a half; there, and where 127 / most leaves float32's range,
+// the quotient is taken in double precision, which tells every half from its
+// neighbours: 254 x and an odd multiple of most, both of at most 32 bits,
+// differ by 2^-32 of themselves or not at all.  Adding 1.5 * 2^23 rounds to
+// the nearest integer and leaves it, as a byte, in the sum's last bits.
 struct RowCoder {
   float most, inv;
   bool easy;
@@ -48,24 +49,43 @@ struct RowCoder {
     easy = most > 1e-30f && most < 1e30f;
     inv = easy ? 127.0f / most : 0.0f;
   }
-  __device__ __forceinline__ bool empty() const { return !(most > 0.0f) || !isfinite(most); }
   // 0 for a row of zeros, NaN for a row that holds an infinity or a NaN: its
   // products are NaN
   __device__ __forceinline__ float scale() const {
     return isfinite(most) ? most / 127.0f : __int_as_float(0x7fc00000);
   }
-  __device__ __forceinline__ int code(float x) const {
-    const float q = x * inv;
-    const float r = rintf(q);
-    if (easy && fabsf(fabsf(q - r) - 0.5f) > 1e-4f) return static_cast<int>(r);
-    if (empty()) return 0;
-    return static_cast<int>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(most)));
+  // (x's code in the last byte, with its distance from x added to `far`)
+  __device__ __forceinline__ uint32_t quick(float x, float& far) const {
+    const float q = x * inv, r = q + 12582912.0f;
+    far = fmaxf(far, fabsf(q - (r - 12582912.0f)));
+    return __float_as_uint(r);
+  }
+  __device__ __noinline__ uint32_t slow(float x) const {
+    if (!(most > 0.0f) || !isfinite(most)) return 0;
+    return static_cast<uint32_t>(
+        static_cast<int>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(most))));
+  }
+  __device__ __forceinline__ uint32_t code(float x) const {
+    float far = 0.0f;
+    const uint32_t c = quick(x, far);
+    return easy && far < 0.4999f ? c : slow(x);
+  }
+  // eight codes, packed
+  __device__ __forceinline__ uint2 codes(const float (&x)[8]) const {
+    uint32_t c[8];
+    float far = easy ? 0.0f : 1.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c[k] = quick(x[k], far);
+    if (far >= 0.4999f) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) c[k] = code(x[k]);
+    }
+    auto four = [&](int k) {
+      return __byte_perm(__byte_perm(c[k], c[k + 1], 0x0040), __byte_perm(c[k + 2], c[k + 3], 0x0040), 0x5410);
+    };
+    return make_uint2(four(0), four(4));
   }
 };
-
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-  return (a & 0xff) | ((b & 0xff) << 8) | ((c & 0xff) << 16) | (static_cast<uint32_t>(d) << 24);
-}
 
 // Eight consecutive elements as floats (16 bytes of bf16, 32 of float32).
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
@@ -95,57 +115,62 @@ __device__ __forceinline__ U from_float(float v) {
 
 }  // namespace
 
+// The largest magnitude among `warps` warps' (all of the block's threads call).
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* part) {
+  v = warp_max(v);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = part[0];
+  for (int k = 1; k < static_cast<int>(blockDim.x >> 5); ++k) v = max(v, part[k]);
+  return v;
+}
+
 // ------------------------------------------------------------ row codes
-// One warp per row.  A lane keeps HOLD groups of eight elements between the
-// search for the largest and the coding; what a longer row has beyond them is
-// read again (from L2).  `wide`: rows start at 16-byte boundaries in both
-// arrays, so groups of eight can move at once.
+// A block of `blockDim.x` threads for each row, as many as give a thread two
+// groups of eight elements, which it keeps between the search for the largest
+// and the coding; what a longer row has beyond them is read again (from L2).
+// `wide`: rows start at 16-byte boundaries in both arrays, so groups of eight
+// can move at once.
 template <typename T>
-__global__ void __launch_bounds__(256) relkl_quantize_rows_kernel(const RowsParams p) {
-  constexpr int HOLD = 8;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
+__global__ void __launch_bounds__(512) relkl_quantize_rows_kernel(const RowsParams p) {
+  constexpr int HOLD = 2;
+  __shared__ uint32_t part[16];
+  const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
   int8_t* q = p.q + row * p.q_stride;
-  const int groups = p.wide ? p.K / 8 : 0;
+  const int groups = p.wide ? p.K / 8 : 0, step = blockDim.x;
   float v[HOLD][8];
   uint32_t most = 0;
 #pragma unroll
-  for (int h = 0; h < HOLD; ++h) {
-    const int g = h * 32 + lane;
-    if (g < groups) {
-      load8(x + 8 * g, v[h]);
+  for (int h = 0; h < HOLD; ++h)
+    if (h * step + threadIdx.x < groups) load8(x + 8 * (h * step + threadIdx.x), v[h]);
+#pragma unroll
+  for (int h = 0; h < HOLD; ++h)
+    if (h * step + threadIdx.x < groups)
 #pragma unroll
       for (int k = 0; k < 8; ++k) most = max(most, magnitude(v[h][k]));
-    }
-  }
-  for (int g = HOLD * 32 + lane; g < groups; g += 32) {
+  for (int g = HOLD * step + threadIdx.x; g < groups; g += step) {
     float w[8];
     load8(x + 8 * g, w);
 #pragma unroll
     for (int k = 0; k < 8; ++k) most = max(most, magnitude(w[k]));
   }
-  for (int i = 8 * groups + lane; i < p.K; i += 32) most = max(most, magnitude(to_float(x[i])));
-  const RowCoder coder(warp_max(most));
-  auto put = [&](int g, const float(&w)[8]) {
-    int c[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) c[k] = coder.code(w[k]);
-    __stcg(reinterpret_cast<uint2*>(q + 8 * g),
-           make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7])));
-  };
+#pragma unroll 4
+  for (int i = 8 * groups + threadIdx.x; i < p.K; i += step) most = max(most, magnitude(to_float(x[i])));
+  const RowCoder coder(block_max(most, part));
 #pragma unroll
   for (int h = 0; h < HOLD; ++h)
-    if (h * 32 + lane < groups) put(h * 32 + lane, v[h]);
-  for (int g = HOLD * 32 + lane; g < groups; g += 32) {
+    if (h * step + threadIdx.x < groups)
+      __stcg(reinterpret_cast<uint2*>(q + 8 * (h * step + threadIdx.x)), coder.codes(v[h]));
+  for (int g = HOLD * step + threadIdx.x; g < groups; g += step) {
     float w[8];
     load8(x + 8 * g, w);
-    put(g, w);
+    __stcg(reinterpret_cast<uint2*>(q + 8 * g), coder.codes(w));
   }
-  for (int i = 8 * groups + lane; i < p.K; i += 32)
+#pragma unroll 4
+  for (int i = 8 * groups + threadIdx.x; i < p.K; i += step)
     q[i] = static_cast<int8_t>(coder.code(to_float(x[i])));
-  if (lane == 0) p.scale[row] = coder.scale();
+  if (threadIdx.x == 0) p.scale[row] = coder.scale();
 }
 
 // ------------------------------------------------------------ few rows
@@ -182,23 +207,13 @@ __global__ void __launch_bounds__(256) relkl_gemv_i8_kernel(const GemvParams p) 
     }
     for (int i = 8 * groups + threadIdx.x; i < p.K; i += 256)
       most = max(most, magnitude(to_float(x[i])));
-    most = warp_max(most);
     __syncthreads();          // the last row's maxima have been read
-    if (lane == 0) part[warp] = most;
-    __syncthreads();
-    most = part[0];
-#pragma unroll
-    for (int k = 1; k < 8; ++k) most = max(most, part[k]);
-    const RowCoder coder(most);
+    const RowCoder coder(block_max(most, part));
     int8_t* q = codes + r * pitch;
     for (int g = threadIdx.x; g < groups; g += 256) {
       float v[8];
       load8(x + 8 * g, v);
-      int k[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) k[i] = coder.code(v[i]);
-      *reinterpret_cast<uint2*>(q + 8 * g) =
-          make_uint2(pack4(k[0], k[1], k[2], k[3]), pack4(k[4], k[5], k[6], k[7]));
+      *reinterpret_cast<uint2*>(q + 8 * g) = coder.codes(v);
     }
     for (int i = 8 * groups + threadIdx.x; i < pitch; i += 256)
       q[i] = i < p.K ? static_cast<int8_t>(coder.code(to_float(x[i]))) : 0;
@@ -261,7 +276,8 @@ struct Smem {
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = 6;
   static constexpr int TURN = STAGES * STAGE;          // epilogue warps' blocks
-  static constexpr int BARS = TURN + 4 * TURN_BYTES;   // full, empty, acc_full, drain
+  static constexpr int SCALES = TURN + 4 * TURN_BYTES;
+  static constexpr int BARS = SCALES + 4 * 2 * BN * 4;   // full, empty, acc_full, drain
   static constexpr int MISC = BARS + (2 * STAGES + 2) * 8;
   static constexpr int ALLOC = MISC + 16 + 1024;
   // a CTA's share of a split sum: 128 rows, padded against bank conflicts
@@ -339,41 +355,80 @@ __device__ __forceinline__ void store_eight(const I8Params& p, int64_t row, int 
   }
 }
 
-// A warp's 32 rows x 32 columns, one row to a lane, are turned through its
-// part of shared memory so that stores run along rows: eight columns to a lane
-// and four lanes to a row where rows of y start at 16-byte boundaries, else one
-// column to a lane.  row0, c0: the first row and column; sx: lane l's row's
-// scale.
+// A warp keeps the scales and biases of its tile's columns in shared memory:
+// n (a multiple of 32) from column c0 on.
+__device__ __forceinline__ void stage_scales(const I8Params& p, float* scales, int c0, int n) {
+  __syncwarp();                                      // the last tile's have been read
+  for (int k = threadIdx.x & 31; k < n; k += 32) {
+    const bool in = c0 + k < p.cols;
+    scales[k] = in ? __ldg(p.w_scale + c0 + k) : 0.0f;
+    scales[n + k] = in && p.bias ? __ldg(p.bias + c0 + k) : 0.0f;
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void store32(void* y, const uint32_t* w) {   // 32 bytes, so aligned
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// A warp's 32 rows x 32 columns, one row to a lane.  Where rows of y start at
+// 32-byte boundaries (y_wide 2) each lane stores whole sectors of its row, at
+// 16-byte boundaries (1) halves of them.  Else the sums are turned through
+// shared memory, and the warp stores one row at a time, a column to a lane.
 template <typename U>
-__device__ __forceinline__ void store_block(const I8Params& p, int* turn, int64_t row0, int c0, float sx,
+__device__ __forceinline__ void store_block(const I8Params& p, int* turn, const float* scales,
+                                            const float* biases, int64_t row, int c0, float sx,
                                             const float (&bits)[32]) {
   const int lane = threadIdx.x & 31;
+  if (p.y_wide && c0 + 32 <= p.cols) {
+    constexpr int W = 32 * sizeof(U) / 4;             // words of the block's row
+    uint32_t w[W];
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      const float4 s = *reinterpret_cast<const float4*>(scales + k);
+      const float4 b = *reinterpret_cast<const float4*>(biases + k);
+      const float v0 = fmaf(static_cast<float>(__float_as_int(bits[k])), sx * s.x, b.x);
+      const float v1 = fmaf(static_cast<float>(__float_as_int(bits[k + 1])), sx * s.y, b.y);
+      const float v2 = fmaf(static_cast<float>(__float_as_int(bits[k + 2])), sx * s.z, b.z);
+      const float v3 = fmaf(static_cast<float>(__float_as_int(bits[k + 3])), sx * s.w, b.w);
+      if constexpr (sizeof(U) == 4) {
+        w[k] = __float_as_uint(v0);
+        w[k + 1] = __float_as_uint(v1);
+        w[k + 2] = __float_as_uint(v2);
+        w[k + 3] = __float_as_uint(v3);
+      } else {
+        w[k / 2] = pack_bf16x2(v0, v1);
+        w[k / 2 + 1] = pack_bf16x2(v2, v3);
+      }
+    }
+    if (row < p.rows) {
+      uint32_t* y = reinterpret_cast<uint32_t*>(static_cast<U*>(p.y) + row * p.y_stride + c0);
+      if (p.y_wide == 2) {
+#pragma unroll
+        for (int k = 0; k < W; k += 8) store32(y + k, w + k);
+      } else {
+#pragma unroll
+        for (int k = 0; k < W; k += 4)
+          *reinterpret_cast<uint4*>(y + k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+      }
+    }
+    return;
+  }
   __syncwarp();                                      // the last block has been read
 #pragma unroll
   for (int k = 0; k < 32; ++k) turn[lane * TURN_PITCH + k] = __float_as_int(bits[k]);
   __syncwarp();
-  if (p.y_wide) {
-    const int c = c0 + (lane & 3) * 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = (lane >> 2) + 8 * i;
-      const float s = __shfl_sync(0xffffffffu, sx, r);
-      int acc[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = turn[r * TURN_PITCH + (lane & 3) * 8 + k];
-      if (row0 + r < p.rows && c < p.cols) store_eight<U>(p, row0 + r, c, s, acc);
-    }
-  } else {
-    const int c = c0 + lane;
-    const bool in = c < p.cols;
-    const float sw = in ? __ldg(p.w_scale + c) : 0.0f, b = in && p.bias ? __ldg(p.bias + c) : 0.0f;
-    U* y = static_cast<U*>(p.y) + c;
+  const float sw = scales[lane], b = biases[lane];
+  const int64_t row0 = row - lane;
+  U* y = static_cast<U*>(p.y) + row0 * p.y_stride + c0 + lane;
+  const int64_t left = p.rows - row0;
 #pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-      const float s = __shfl_sync(0xffffffffu, sx, r);
-      const float v = fmaf(static_cast<float>(turn[r * TURN_PITCH + lane]), s * sw, b);
-      if (in && row0 + r < p.rows) y[(row0 + r) * p.y_stride] = from_float<U>(v);
-    }
+  for (int r = 0; r < 32; ++r) {
+    const float s = __shfl_sync(0xffffffffu, sx, r);
+    const float v = fmaf(static_cast<float>(turn[r * TURN_PITCH + lane]), s * sw, b);
+    if (r < left && c0 + lane < p.cols) y[r * p.y_stride] = from_float<U>(v);
   }
 }
 
@@ -470,7 +525,9 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
   const bool live = warp >= 2 && row < p.rows;
   const float sx = live ? p.x_scale[row] : 0.0f;
   int* turn = reinterpret_cast<int*>(gbase + S::TURN + (warp & 3) * TURN_BYTES);
+  float* scales = reinterpret_cast<float*>(gbase + S::SCALES) + (warp & 3) * 2 * BN;
   if (warp >= 2) {
+    if (p.split == 1) stage_scales(p, scales, nt * BN, BN);
     bool ok = mbar_wait(ACC, 0, wc, W_EPI_P_FULL);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
@@ -482,7 +539,8 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
         tmem_ld32(addr + c, bits);
         tmem_wait_ld();
         if (p.split == 1) {
-          if (nt * BN + c < p.cols) store_block<U>(p, turn, row - lane, nt * BN + c, sx, bits);
+          if (nt * BN + c < p.cols)
+            store_block<U>(p, turn, scales + c, scales + BN + c, row, nt * BN + c, sx, bits);
         } else {
           const uint32_t dst = base + ((q * 32 + lane) * S::PITCH + c) * 4;
 #pragma unroll
@@ -533,13 +591,18 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
 // while the next one's are formed.
 namespace i8 {
 
+// warp 0 TMA, warp 1 MMA, warps 2-9 epilogue: two for each quarter of the
+// TMEM lanes, one for each half of the columns
+constexpr int PAIR_EPI = 8, PAIR_THREADS = 64 + 32 * PAIR_EPI;
+
 template <int BN>
 struct PairSmem {
   static constexpr int A_BYTES = BM * BK, B_BYTES = BN / 2 * BK;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int STAGES = 5;
   static constexpr int TURN = STAGES * STAGE;
-  static constexpr int BARS = TURN + 4 * TURN_BYTES;   // full, empty, acc_full[2], acc_empty[2], drain
+  static constexpr int SCALES = TURN + PAIR_EPI * TURN_BYTES;
+  static constexpr int BARS = SCALES + PAIR_EPI * BN * 4;   // full, empty, acc_full[2], acc_empty[2], drain
   static constexpr int MISC = BARS + (2 * STAGES + 5) * 8;
   static constexpr int ALLOC = MISC + 16 + 1024;
   static_assert(ALLOC <= 232448, "shared memory exceeds 227 KB");
@@ -631,7 +694,7 @@ __device__ __forceinline__ void pair_unit(const I8Params& p, int unit, int& mt, 
 }  // namespace i8
 
 template <int BN, typename U>
-__global__ void __launch_bounds__(i8::THREADS, 1)
+__global__ void __launch_bounds__(i8::PAIR_THREADS, 1)
 relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
   using namespace i8;
   using S = PairSmem<BN>;
@@ -658,7 +721,7 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(ACC_FULL(b), 1);
-      mbar_init(ACC_EMPTY(b), 8);      // the epilogue warps of both CTAs
+      mbar_init(ACC_EMPTY(b), 2 * PAIR_EPI);   // the epilogue warps of both CTAs
     }
     mbar_init(DRAIN, 1);
     *abort_flag = 0;
@@ -744,29 +807,38 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
     }
     __syncwarp();
   } else {
-    const int q = warp & 3;
-    int* turn = reinterpret_cast<int*>(gbase + S::TURN + q * TURN_BYTES);
-    const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
+    const int q = warp & 3, epi = warp - 2;
+    int* turn = reinterpret_cast<int*>(gbase + S::TURN + epi * TURN_BYTES);
+    float* scales = reinterpret_cast<float*>(gbase + S::SCALES) + epi * BN;   // and biases
+    constexpr int COLS = BN / 2;
+    const int half = (epi >> 2) * COLS;
+    const uint32_t lane_addr = (static_cast<uint32_t>(q * 32) << 16) + half;
     uint32_t nacc = 0;
     for (int unit = first; unit < p.n_units; unit += stride, ++nacc) {
       int mt, nt;
       pair_unit(p, unit, mt, nt);
       const int ab = nacc & 1;
-      const int64_t row0 = static_cast<int64_t>(mt) * 2 * BM + rank * BM + q * 32;
-      const float sx = row0 + lane < p.rows ? p.x_scale[row0 + lane] : 0.0f;
+      const int64_t row = static_cast<int64_t>(mt) * 2 * BM + rank * BM + q * 32 + lane;
+      const int col = nt * BN + half;
+      const float sx = row < p.rows ? __ldg(p.x_scale + row) : 0.0f;
+      stage_scales(p, scales, col, COLS);
       if (!mbar_wait_warp(ACC_FULL(ab), (nacc >> 1) & 1, wc, W_EPI_P_FULL)) break;
       tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        float bits[32];
-        tmem_ld32(tmem + lane_addr + ab * BN + c, bits);
+      float bits[2][32];
+      const uint32_t acc = tmem + lane_addr + ab * BN;
+      tmem_ld32(acc, bits[0]);
+#pragma unroll
+      for (int k = 0; k < COLS / 32; ++k) {
         tmem_wait_ld();
-        if (c == BN - 32) {
+        if (k + 1 < COLS / 32) {
+          tmem_ld32(acc + 32 * (k + 1), bits[(k + 1) & 1]);
+        } else {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_peer(peer(ACC_EMPTY(ab), 0));
         }
-        if (nt * BN + c < p.cols) store_block<U>(p, turn, row0, nt * BN + c, sx, bits);
+        if (col + 32 * k < p.cols)
+          store_block<U>(p, turn, scales + 32 * k, scales + COLS + 32 * k, row, col + 32 * k, sx, bits[k & 1]);
       }
     }
     __syncwarp();
@@ -784,12 +856,14 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
 
 // ------------------------------------------------------------- launches
 cudaError_t launch_quantize_rows(const RowsParams& p, bool x_bf16, cudaStream_t stream) {
-  const int64_t blocks = (p.rows + 7) / 8;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (p.rows > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  // two groups of eight elements to a thread, 32 to 512 threads
+  int threads = (p.K + 511) / 512 * 32;
+  threads = threads > 512 ? 512 : threads;
   if (x_bf16)
-    relkl_quantize_rows_kernel<__nv_bfloat16><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
+    relkl_quantize_rows_kernel<__nv_bfloat16><<<static_cast<unsigned>(p.rows), threads, 0, stream>>>(p);
   else
-    relkl_quantize_rows_kernel<float><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
+    relkl_quantize_rows_kernel<float><<<static_cast<unsigned>(p.rows), threads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -825,11 +899,11 @@ bool encode_codes(CUtensorMap* m, const int8_t* q, int64_t rows, int K, int64_t 
 }
 
 template <typename K>
-cudaError_t launch_cluster(K kernel, const I8Params& p, unsigned grid, int cluster, int smem,
-                           cudaStream_t stream) {
+cudaError_t launch_cluster(K kernel, const I8Params& p, unsigned grid, int threads, int cluster,
+                           int smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(i8::THREADS);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -854,7 +928,7 @@ cudaError_t gemm(I8Params& p, const I8Call& c, cudaStream_t stream) {
   auto* kernel = relkl_gemm_i8_kernel<BN, U>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::ALLOC);
   if (e != cudaSuccess) return e;
-  return launch_cluster(kernel, p, static_cast<unsigned>(tiles * p.split), p.split, S::ALLOC, stream);
+  return launch_cluster(kernel, p, static_cast<unsigned>(tiles * p.split), i8::THREADS, p.split, S::ALLOC, stream);
 }
 
 template <int BN, typename U>
@@ -872,7 +946,7 @@ cudaError_t gemm_pair(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::ALLOC);
   if (e != cudaSuccess) return e;
   const int pairs = p.n_units < num_sms / 2 ? p.n_units : num_sms / 2;
-  return launch_cluster(kernel, p, 2 * pairs, 2, S::ALLOC, stream);
+  return launch_cluster(kernel, p, 2 * pairs, i8::PAIR_THREADS, 2, S::ALLOC, stream);
 }
 
 template <typename U>

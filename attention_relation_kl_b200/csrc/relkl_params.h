@@ -184,7 +184,7 @@ struct I8Params {
   void* y;
   int64_t rows, y_stride;
   int cols;
-  int y_wide;                         // rows of y start at 16-byte boundaries
+  int y_wide;                         // rows of y start at 16-byte (1) or 32-byte (2) boundaries
   int m_tiles, n_tiles, n_units, k_chunks, split;   // set by the launch
   DevStatus* status;
   unsigned long long timeout_ns;
