@@ -42,7 +42,7 @@ cudaError_t launch_grad_norm(const NormTensor* t, int n, int64_t chunks, int gri
                              float* out, float max_norm, cudaStream_t stream);
 cudaError_t launch_norm_finish(const double* partial, int n, float max_norm, float* out,
                                cudaStream_t stream);
-cudaError_t launch_quantize_rows(const RowsParams& p, bool x_bf16, cudaStream_t stream);
+cudaError_t launch_quantize_rows(const RowsParams& p, bool x_bf16, int num_sms, cudaStream_t stream);
 cudaError_t launch_gemv_i8(const GemvParams& p, bool x_bf16, bool y_bf16, cudaStream_t stream);
 cudaError_t launch_gemm_i8(I8Params& p, const I8Call& c, bool y_bf16, int num_sms, cudaStream_t stream);
 using EncodeTiledFnG = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -366,9 +366,10 @@ bool few_rows(int64_t rows, int32_t K) {
 relkl_status matmul_i8(int64_t rows, int32_t cols, int32_t K, const int8_t* q, int64_t q_stride,
                        const float* q_scale, const int8_t* w, int64_t w_stride,
                        const float* w_scale, const float* bias, void* y, int32_t y_dtype,
-                       int64_t y_stride, void* ws, const DevInfo& dev, cudaStream_t stream) {
+                       int64_t y_stride, void* ws, bool after_rows, const DevInfo& dev,
+                       cudaStream_t stream) {
   if (dev.major != 10) return RELKL_ERR_UNSUPPORTED;
-  I8Call c = {q, w, q_stride, w_stride, K, encode_fn()};
+  I8Call c = {q, w, q_stride, w_stride, K, after_rows, encode_fn()};
   if (!c.encode) return RELKL_ERR_CUDA;
   I8Params p;
   std::memset(&p, 0, sizeof(p));
@@ -387,9 +388,10 @@ relkl_status matmul_i8(int64_t rows, int32_t cols, int32_t K, const int8_t* q, i
 }
 
 relkl_status quantize_rows(int64_t rows, int32_t K, const void* x, int32_t x_dtype, int64_t x_stride,
-                           int8_t* q, int64_t q_stride, float* scale, cudaStream_t stream) {
+                           int8_t* q, int64_t q_stride, float* scale, const DevInfo& dev,
+                           cudaStream_t stream) {
   RowsParams p = {x, q, scale, rows, x_stride, q_stride, K, wide_rows(x, x_dtype, x_stride)};
-  cudaError_t e = launch_quantize_rows(p, x_dtype == RELKL_BF16, stream);
+  cudaError_t e = launch_quantize_rows(p, x_dtype == RELKL_BF16, dev.sms, stream);
   return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
 }
 
@@ -995,7 +997,10 @@ relkl_status relkl_quantize_rows(int64_t rows, int32_t K, const void* x, int32_t
   if (rows == 0) return RELKL_OK;
   if (!matrix_ok(x, x_dtype, x_stride, K) || !codes_ok(q, q_stride, K) || !scale || !aligned(scale, 4))
     return RELKL_ERR_INVALID;
-  return quantize_rows(rows, K, x, x_dtype, x_stride, q, q_stride, scale,
+  relkl_status s;
+  DevInfo dev;
+  if ((s = device_info(&dev)) != RELKL_OK) return s;
+  return quantize_rows(rows, K, x, x_dtype, x_stride, q, q_stride, scale, dev,
                        static_cast<cudaStream_t>(stream));
 }
 
@@ -1015,7 +1020,7 @@ relkl_status relkl_matmul_i8(int64_t rows, int32_t cols, int32_t K, const int8_t
   DevInfo dev;
   if ((s = device_info(&dev)) != RELKL_OK) return s;
   return matmul_i8(rows, cols, K, q, q_stride, q_scale, w, w_stride, w_scale, bias, y, y_dtype,
-                   y_stride, ws, dev, static_cast<cudaStream_t>(stream));
+                   y_stride, ws, false, dev, static_cast<cudaStream_t>(stream));
 }
 
 size_t relkl_linear_i8_bytes(int64_t rows, int32_t K) {
@@ -1050,9 +1055,9 @@ relkl_status relkl_linear_i8(int64_t rows, int32_t cols, int32_t K, const void* 
   int8_t* q = static_cast<int8_t*>(scratch);
   const int64_t pitch = code_pitch(K);
   float* scale = reinterpret_cast<float*>(q + rows * pitch);
-  if ((s = quantize_rows(rows, K, x, x_dtype, x_stride, q, pitch, scale, st)) != RELKL_OK) return s;
+  if ((s = quantize_rows(rows, K, x, x_dtype, x_stride, q, pitch, scale, dev, st)) != RELKL_OK) return s;
   return matmul_i8(rows, cols, K, q, pitch, scale, w, w_stride, w_scale, bias, y, y_dtype, y_stride,
-                   ws, dev, st);
+                   ws, true, dev, st);
 }
 
 relkl_status relkl_cast_bf16(const float* src, void* dst, int64_t n, void* stream) {

@@ -34,51 +34,76 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162f
 // The magnitude's bits order as the magnitudes do, with NaN above infinity.
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// rint(127 x / most), exactly.  The float32 product x (127 / most) is off by
-// less than 127 * 2^-22, so its nearest integer is the code unless it lies
-// within 1e-4 of a half; there, and where 127 / most leaves float32's range,
+// rint(127 x / most), exactly, ties to even.
+//
+// Quick way: x times a number next to 127 / most, added to 1.5 * 2^23 in one
+// fma, which rounds it to the nearest integer and leaves that, as a byte, in
+// the sum's last bits.
+//   * bf16: x = a 2^i and most = b 2^j with a, b < 256, so a quotient v that is
+//     no half n + 1/2 is at least v / (254 a) = 1.5e-5 v away from every half,
+//     and a factor off by 2^-23 of itself cannot carry it across.  Halves occur
+//     where 254 a 2^(i - j) = (2n + 1) b: with b = 254 or 127, when 127 / most
+//     is a power of two and the product exact, and at v = 63.5, where 64 is
+//     right.  The factor rounded up gives all of these.
+//   * float32: a factor just above and one just below.  Where they agree the
+//     quotient between them has that code; they differ only within 2^-21 of
+//     itself of a half, and then code() decides.
+// code(): the nearest integers of x (127 / most), off by less than 127 * 2^-23
+// = 1.6e-5, are told apart by the sign of 254 |x| - (2n + 1) most; both
+// products have at most 32 bits, so each is held exactly as a float and its
+// rest, and so is their difference.  Where 127 / most leaves float32's range
 // the quotient is taken in double precision, which tells every half from its
-// neighbours: 254 x and an odd multiple of most, both of at most 32 bits,
-// differ by 2^-32 of themselves or not at all.  Adding 1.5 * 2^23 rounds to
-// the nearest integer and leaves it, as a byte, in the sum's last bits.
+// neighbours.
 struct RowCoder {
-  float most, inv;
+  static constexpr float kNear = 0.5f - 2e-5f;
+  float most, inv, above;
   bool easy;
   __device__ __forceinline__ explicit RowCoder(uint32_t bits) {
     most = __uint_as_float(bits);
     easy = most > 1e-30f && most < 1e30f;
     inv = easy ? 127.0f / most : 0.0f;
+    above = easy ? __fdiv_ru(127.0f, most) : 0.0f;
   }
   // 0 for a row of zeros, NaN for a row that holds an infinity or a NaN: its
   // products are NaN
   __device__ __forceinline__ float scale() const {
     return isfinite(most) ? most / 127.0f : __int_as_float(0x7fc00000);
   }
-  // (x's code in the last byte, with its distance from x added to `far`)
-  __device__ __forceinline__ uint32_t quick(float x, float& far) const {
-    const float q = x * inv, r = q + 12582912.0f;
-    far = fmaxf(far, fabsf(q - (r - 12582912.0f)));
-    return __float_as_uint(r);
+  // the code of any x
+  __device__ __forceinline__ int code(float x) const {
+    if (!easy) {
+      if (!(most > 0.0f) || !isfinite(most)) return 0;
+      return static_cast<int>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(most)));
+    }
+    const float q = x * inv, r = rintf(q);
+    if (fabsf(q - r) < kNear) return static_cast<int>(r);
+    const float ax = fabsf(x), n = floorf(ax * inv), odd = 2.0f * n + 1.0f;
+    const float p = 254.0f * ax, t = odd * most;
+    const float diff = (p - t) + (fmaf(254.0f, ax, -p) - fmaf(odd, most, -t));
+    const int low = static_cast<int>(n);
+    const int up = diff > 0.0f || (diff == 0.0f && (low & 1));
+    return x < 0.0f ? -(low + up) : low + up;
   }
-  __device__ __noinline__ uint32_t slow(float x) const {
-    if (!(most > 0.0f) || !isfinite(most)) return 0;
-    return static_cast<uint32_t>(
-        static_cast<int>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(most))));
-  }
-  __device__ __forceinline__ uint32_t code(float x) const {
-    float far = 0.0f;
-    const uint32_t c = quick(x, far);
-    return easy && far < 0.4999f ? c : slow(x);
-  }
-  // eight codes, packed
-  __device__ __forceinline__ uint2 codes(const float (&x)[8]) const {
+  // The codes of a group of eight, packed, from the quick way alone; `again`
+  // where they have to be looked at by code().
+  template <typename H>
+  __device__ __forceinline__ uint2 codes(const H& held, bool& again) const {
+    float x[8];
+    held.get(x);
     uint32_t c[8];
-    float far = easy ? 0.0f : 1.0f;
+    again = !easy;
+    if constexpr (H::kBits == 16) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) c[k] = quick(x[k], far);
-    if (far >= 0.4999f) {
+      for (int k = 0; k < 8; ++k) c[k] = __float_as_uint(fmaf(x[k], above, 12582912.0f));
+    } else {
+      const float up = inv * (1.0f + 0x1p-22f), down = inv * (1.0f - 0x1p-22f);
+      uint32_t differ = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) c[k] = code(x[k]);
+      for (int k = 0; k < 8; ++k) {
+        c[k] = __float_as_uint(fmaf(x[k], up, 12582912.0f));
+        differ |= c[k] ^ __float_as_uint(fmaf(x[k], down, 12582912.0f));
+      }
+      again = again || differ != 0;
     }
     auto four = [&](int k) {
       return __byte_perm(__byte_perm(c[k], c[k + 1], 0x0040), __byte_perm(c[k + 2], c[k + 3], 0x0040), 0x5410);
@@ -87,20 +112,55 @@ struct RowCoder {
   }
 };
 
-// Eight consecutive elements as floats (16 bytes of bf16, 32 of float32).
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 w = __ldcg(reinterpret_cast<const uint4*>(p));
-  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+// Eight elements as they are held between two uses.
+template <typename T>
+struct Held;
+template <>
+struct Held<__nv_bfloat16> {
+  static constexpr int kBits = 16;
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = __ldcg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(a[i] << 16);
-    v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    }
   }
+};
+template <>
+struct Held<float> {
+  static constexpr int kBits = 32;
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcg(reinterpret_cast<const float4*>(p));
+    b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+// The largest magnitude so far, as the bits of a float or, for bf16, of two
+// halves of which the larger counts.
+__device__ __forceinline__ uint32_t largest(const Held<float>& h, uint32_t most) {
+  most = max(most, max(max(magnitude(h.a.x), magnitude(h.a.y)), max(magnitude(h.a.z), magnitude(h.a.w))));
+  return max(most, max(max(magnitude(h.b.x), magnitude(h.b.y)), max(magnitude(h.b.z), magnitude(h.b.w))));
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ uint32_t largest(const Held<__nv_bfloat16>& h, uint32_t most) {
+  constexpr uint32_t M = 0x7fff7fffu;
+  return __vmaxu2(__vmaxu2(__vmaxu2(most, h.w.x & M), h.w.y & M), __vmaxu2(h.w.z & M, h.w.w & M));
+}
+__device__ __forceinline__ uint32_t largest(float x, uint32_t most) { return max(most, magnitude(x)); }
+__device__ __forceinline__ uint32_t largest(__nv_bfloat16 x, uint32_t most) {
+  return __vmaxu2(most, __bfloat16_as_ushort(x) & 0x7fffu);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t largest_bits(uint32_t most) {
+  if constexpr (sizeof(T) == 4) return most;
+  return max(most & 0xffff0000u, most << 16);
 }
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
@@ -115,6 +175,9 @@ __device__ __forceinline__ U from_float(float v) {
 
 }  // namespace
 
+// groups of eight of a row that one thread holds
+constexpr int kRowGroups = 4;
+
 // The largest magnitude among `warps` warps' (all of the block's threads call).
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* part) {
   v = warp_max(v);
@@ -126,51 +189,69 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* part) {
 }
 
 // ------------------------------------------------------------ row codes
-// A block of `blockDim.x` threads for each row, as many as give a thread two
-// groups of eight elements, which it keeps between the search for the largest
-// and the coding; what a longer row has beyond them is read again (from L2).
+// A team of threads for each row, as many as give each kRowGroups groups of
+// eight elements of it: a warp of eight (WARPS), or a block.  The groups stay
+// in registers between the search for the largest and the coding; what a longer
+// row has beyond them is read again (from L2).
 // `wide`: rows start at 16-byte boundaries in both arrays, so groups of eight
-// can move at once.
-template <typename T>
-__global__ void __launch_bounds__(512) relkl_quantize_rows_kernel(const RowsParams p) {
-  constexpr int HOLD = 2;
+// can move at once.  32K rows of 4096 bf16: 64 us, 6.3 TB/s; with 2 or 8 groups
+// to a thread 94 and 72 us.
+template <typename T, bool WARPS>
+__global__ void __launch_bounds__(512, 2) relkl_quantize_rows_kernel(const RowsParams p) {
+  constexpr int HOLD = kRowGroups;
   __shared__ uint32_t part[16];
-  const int64_t row = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int64_t row = WARPS ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARPS && row >= p.rows) return;
+  const int me = WARPS ? threadIdx.x & 31 : threadIdx.x, step = WARPS ? 32 : blockDim.x;
   const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
   int8_t* q = p.q + row * p.q_stride;
-  const int groups = p.wide ? p.K / 8 : 0, step = blockDim.x;
-  float v[HOLD][8];
+  const int groups = p.wide ? p.K / 8 : 0;
+  Held<T> v[HOLD];
+#pragma unroll
+  for (int h = 0; h < HOLD; ++h)
+    if (h * step + me < groups) v[h].load(x + 8 * (h * step + me));
   uint32_t most = 0;
 #pragma unroll
   for (int h = 0; h < HOLD; ++h)
-    if (h * step + threadIdx.x < groups) load8(x + 8 * (h * step + threadIdx.x), v[h]);
-#pragma unroll
-  for (int h = 0; h < HOLD; ++h)
-    if (h * step + threadIdx.x < groups)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) most = max(most, magnitude(v[h][k]));
-  for (int g = HOLD * step + threadIdx.x; g < groups; g += step) {
-    float w[8];
-    load8(x + 8 * g, w);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) most = max(most, magnitude(w[k]));
+    if (h * step + me < groups) most = largest(v[h], most);
+  for (int g = HOLD * step + me; g < groups; g += step) {
+    Held<T> h;
+    h.load(x + 8 * g);
+    most = largest(h, most);
   }
 #pragma unroll 4
-  for (int i = 8 * groups + threadIdx.x; i < p.K; i += step) most = max(most, magnitude(to_float(x[i])));
-  const RowCoder coder(block_max(most, part));
+  for (int i = 8 * groups + me; i < p.K; i += step) most = largest(x[i], most);
+  const RowCoder coder(WARPS ? warp_max(largest_bits<T>(most)) : block_max(largest_bits<T>(most), part));
+  // groups with a code near a half, in the order of this thread's groups: few,
+  // so they are done once more behind the others, element by element
+  uint32_t redo = 0;
 #pragma unroll
   for (int h = 0; h < HOLD; ++h)
-    if (h * step + threadIdx.x < groups)
-      __stcg(reinterpret_cast<uint2*>(q + 8 * (h * step + threadIdx.x)), coder.codes(v[h]));
-  for (int g = HOLD * step + threadIdx.x; g < groups; g += step) {
-    float w[8];
-    load8(x + 8 * g, w);
-    __stcg(reinterpret_cast<uint2*>(q + 8 * g), coder.codes(w));
+    if (h * step + me < groups) {
+      bool again;
+      __stcg(reinterpret_cast<uint2*>(q + 8 * (h * step + me)), coder.codes(v[h], again));
+      redo |= static_cast<uint32_t>(again) << h;
+    }
+  while (redo) {
+    const int g = (__ffs(redo) - 1) * step + me;
+    redo &= redo - 1;
+#pragma unroll 1
+    for (int k = 8 * g; k < 8 * g + 8; ++k) q[k] = static_cast<int8_t>(coder.code(to_float(x[k])));
   }
-#pragma unroll 4
-  for (int i = 8 * groups + threadIdx.x; i < p.K; i += step)
+  for (int g = HOLD * step + me; g < groups; g += step) {
+    Held<T> h;
+    h.load(x + 8 * g);
+    bool again;
+    __stcg(reinterpret_cast<uint2*>(q + 8 * g), coder.codes(h, again));
+    if (again)
+#pragma unroll 1
+      for (int k = 8 * g; k < 8 * g + 8; ++k) q[k] = static_cast<int8_t>(coder.code(to_float(x[k])));
+  }
+#pragma unroll 1
+  for (int i = 8 * groups + me; i < p.K; i += step)
     q[i] = static_cast<int8_t>(coder.code(to_float(x[i])));
-  if (threadIdx.x == 0) p.scale[row] = coder.scale();
+  if (me == 0) p.scale[row] = coder.scale();
 }
 
 // ------------------------------------------------------------ few rows
@@ -200,20 +281,23 @@ __global__ void __launch_bounds__(256) relkl_gemv_i8_kernel(const GemvParams p) 
     uint32_t most = 0;
     const int groups = p.wide ? p.K / 8 : 0;
     for (int g = threadIdx.x; g < groups; g += 256) {
-      float v[8];
-      load8(x + 8 * g, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) most = max(most, magnitude(v[k]));
+      Held<T> h;
+      h.load(x + 8 * g);
+      most = largest(h, most);
     }
     for (int i = 8 * groups + threadIdx.x; i < p.K; i += 256)
-      most = max(most, magnitude(to_float(x[i])));
+      most = largest(x[i], most);
     __syncthreads();          // the last row's maxima have been read
-    const RowCoder coder(block_max(most, part));
+    const RowCoder coder(block_max(largest_bits<T>(most), part));
     int8_t* q = codes + r * pitch;
     for (int g = threadIdx.x; g < groups; g += 256) {
-      float v[8];
-      load8(x + 8 * g, v);
-      *reinterpret_cast<uint2*>(q + 8 * g) = coder.codes(v);
+      Held<T> h;
+      h.load(x + 8 * g);
+      bool again;
+      *reinterpret_cast<uint2*>(q + 8 * g) = coder.codes(h, again);
+      if (again)
+#pragma unroll 1
+        for (int k = 8 * g; k < 8 * g + 8; ++k) q[k] = static_cast<int8_t>(coder.code(to_float(x[k])));
     }
     for (int i = 8 * groups + threadIdx.x; i < pitch; i += 256)
       q[i] = i < p.K ? static_cast<int8_t>(coder.code(to_float(x[i]))) : 0;
@@ -304,6 +388,10 @@ __device__ __forceinline__ void mma_lead(uint32_t leader, uint32_t d_tmem, uint3
       "r"(a_lo), "r"(b_lo), "r"(hi), "r"(id), "r"(accumulate), "r"(leader)
       : "memory");
 }
+
+// Waits for the kernel before this one where this one was started ahead of its
+// end (the coding of the rows; elsewhere it returns at once).
+__device__ __forceinline__ void rows_are_coded() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -483,7 +571,18 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
   if (warp == 0) {
     if (lane == 0) {
       uint32_t arms[S::STAGES] = {};
-      for (int kc = k0, it = 0; kc < k1; ++kc, ++it) {
+      // the weights of the first stages, which no kernel before this one
+      // writes, are on their way while the rows are still being coded
+      const int early = min(k1 - k0, S::STAGES);
+      for (int it = 0; it < early; ++it) {
+        mbar_arrive_expect_tx(FULL(it), S::STAGE);
+        tma_load_2d(base + it * S::STAGE + S::A_BYTES, &p.tm_b, FULL(it), (k0 + it) * BK, nt * BN);
+        ++arms[it];
+      }
+      rows_are_coded();
+      for (int it = 0; it < early; ++it)
+        tma_load_2d(base + it * S::STAGE, &p.tm_a, FULL(it), (k0 + it) * BK, mt * BM);
+      for (int kc = k0 + early, it = early; kc < k1; ++kc, ++it) {
         const int s = it % S::STAGES;
         if (!mbar_wait(EMPTY(s), ((it / S::STAGES) & 1) ^ 1, wc, W_TMA_EMPTY_J)) break;
         const uint32_t a = base + s * S::STAGE;
@@ -523,6 +622,7 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
   const int q = warp & 3;      // TMEM lane quarter of an epilogue warp
   const int64_t row = static_cast<int64_t>(mt) * BM + q * 32 + lane;
   const bool live = warp >= 2 && row < p.rows;
+  if (warp >= 2) rows_are_coded();
   const float sx = live ? p.x_scale[row] : 0.0f;
   int* turn = reinterpret_cast<int*>(gbase + S::TURN + (warp & 3) * TURN_BYTES);
   float* scales = reinterpret_cast<float*>(gbase + S::SCALES) + (warp & 3) * 2 * BN;
@@ -748,12 +848,25 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
       uint32_t it = 0;
       uint32_t arms[S::STAGES] = {};
       bool ok = true;
+      int early = 0;
       for (int unit = first; ok && unit < p.n_units; unit += stride) {
         int mt, nt;
         pair_unit(p, unit, mt, nt);
         const int row = mt * 2 * BM + static_cast<int>(rank) * BM;
         const int col = nt * BN + static_cast<int>(rank) * (BN / 2);
-        for (int kc = 0; kc < p.k_chunks; ++kc, ++it) {
+        if (unit == first) {      // weights before the rows are coded, as above
+          early = min(p.k_chunks, S::STAGES);
+          for (int s = 0; s < early; ++s) {
+            if (rank == 0) mbar_arrive_expect_tx(FULL(s), 2 * S::STAGE);
+            load_pair(base + s * S::STAGE + S::A_BYTES, &p.tm_b, peer(FULL(s), 0), s * BK, col);
+            ++arms[s];
+          }
+          rows_are_coded();
+          for (int s = 0; s < early; ++s)
+            load_pair(base + s * S::STAGE, &p.tm_a, peer(FULL(s), 0), s * BK, row);
+          it = early;
+        }
+        for (int kc = unit == first ? early : 0; kc < p.k_chunks; ++kc, ++it) {
           const int s = it % S::STAGES;
           if (!(ok = mbar_wait(EMPTY(s), ((it / S::STAGES) & 1) ^ 1, wc, W_TMA_EMPTY_J))) break;
           const uint32_t a = base + s * S::STAGE;
@@ -814,6 +927,7 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
     const int half = (epi >> 2) * COLS;
     const uint32_t lane_addr = (static_cast<uint32_t>(q * 32) << 16) + half;
     uint32_t nacc = 0;
+    rows_are_coded();
     for (int unit = first; unit < p.n_units; unit += stride, ++nacc) {
       int mt, nt;
       pair_unit(p, unit, mt, nt);
@@ -855,16 +969,24 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
 }
 
 // ------------------------------------------------------------- launches
-cudaError_t launch_quantize_rows(const RowsParams& p, bool x_bf16, cudaStream_t stream) {
-  if (p.rows > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  // two groups of eight elements to a thread, 32 to 512 threads
-  int threads = (p.K + 511) / 512 * 32;
+namespace {
+
+template <typename T>
+cudaError_t quantize_rows(const RowsParams& p, int num_sms, cudaStream_t stream) {
+  constexpr int one = 8 * kRowGroups * 32;   // a warp's elements
+  int threads = (p.K + one - 1) / one * 32;
   threads = threads > 512 ? 512 : threads;
-  if (x_bf16)
-    relkl_quantize_rows_kernel<__nv_bfloat16><<<static_cast<unsigned>(p.rows), threads, 0, stream>>>(p);
+  if (threads == 32)
+    relkl_quantize_rows_kernel<T, true><<<static_cast<unsigned>((p.rows + 7) / 8), 256, 0, stream>>>(p);
   else
-    relkl_quantize_rows_kernel<float><<<static_cast<unsigned>(p.rows), threads, 0, stream>>>(p);
+    relkl_quantize_rows_kernel<T, false><<<static_cast<unsigned>(p.rows), threads, 0, stream>>>(p);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const RowsParams& p, bool x_bf16, int num_sms, cudaStream_t stream) {
+  return x_bf16 ? quantize_rows<__nv_bfloat16>(p, num_sms, stream) : quantize_rows<float>(p, num_sms, stream);
 }
 
 namespace {
@@ -900,19 +1022,21 @@ bool encode_codes(CUtensorMap* m, const int8_t* q, int64_t rows, int K, int64_t 
 
 template <typename K>
 cudaError_t launch_cluster(K kernel, const I8Params& p, unsigned grid, int threads, int cluster,
-                           int smem, cudaStream_t stream) {
+                           int smem, bool ahead, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ahead ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -928,7 +1052,7 @@ cudaError_t gemm(I8Params& p, const I8Call& c, cudaStream_t stream) {
   auto* kernel = relkl_gemm_i8_kernel<BN, U>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::ALLOC);
   if (e != cudaSuccess) return e;
-  return launch_cluster(kernel, p, static_cast<unsigned>(tiles * p.split), i8::THREADS, p.split, S::ALLOC, stream);
+  return launch_cluster(kernel, p, static_cast<unsigned>(tiles * p.split), i8::THREADS, p.split, S::ALLOC, c.after_rows, stream);
 }
 
 template <int BN, typename U>
@@ -946,7 +1070,7 @@ cudaError_t gemm_pair(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::ALLOC);
   if (e != cudaSuccess) return e;
   const int pairs = p.n_units < num_sms / 2 ? p.n_units : num_sms / 2;
-  return launch_cluster(kernel, p, 2 * pairs, i8::PAIR_THREADS, 2, S::ALLOC, stream);
+  return launch_cluster(kernel, p, 2 * pairs, i8::PAIR_THREADS, 2, S::ALLOC, c.after_rows, stream);
 }
 
 template <typename U>

@@ -199,6 +199,7 @@ struct I8Call {
   const int8_t *q, *w;
   int64_t q_stride, w_stride;
   int K;
+  bool after_rows;   // the kernel before is the coding of q: start ahead of its end
   EncodeTiled encode;
 };
 

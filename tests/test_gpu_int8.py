@@ -107,6 +107,20 @@ def test_codes_of_ties_extremes_and_rows_without_a_scale(dtype):
     assert torch.equal(y.view(torch.int32), z[:8].view(torch.int32))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_codes_of_every_pair_of_bf16_mantissas(dtype):
+    # a row for each mantissa of its largest element, with every bf16 number down to 2^-12
+    # of it: every half that bf16 numbers can make is there
+    b = torch.arange(128, 256, dtype=torch.float32)
+    x = torch.cat([b * 2.0 ** -e for e in range(13)])
+    rows = torch.where(x[None, :] <= b[:, None], x[None, :], 0.0)
+    rows = torch.cat((rows, -rows), 1)
+    for scale in (1.0, 2.0 ** -60, 2.0 ** 90, 2.0 ** -120):
+        y = (rows * scale).to(dtype).cuda()
+        q, _ = rk.relkl_quantize_rows(y)
+        assert np.array_equal(_np(q), _codes(y)[0])
+
+
 ROWS = [1, 2, 4, 5, 8, 9, 16, 77, 128, 129, 300]
 
 
