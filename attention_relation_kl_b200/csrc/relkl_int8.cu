@@ -443,17 +443,30 @@ __device__ __forceinline__ void store_eight(const I8Params& p, int64_t row, int 
   }
 }
 
-// A warp keeps the scales and biases of its tile's columns in shared memory:
-// n (a multiple of 32) from column c0 on.
-__device__ __forceinline__ void stage_scales(const I8Params& p, float* scales, int c0, int n) {
-  __syncwarp();                                      // the last tile's have been read
-  for (int k = threadIdx.x & 31; k < n; k += 32) {
-    const bool in = c0 + k < p.cols;
-    scales[k] = in ? __ldg(p.w_scale + c0 + k) : 0.0f;
-    scales[n + k] = in && p.bias ? __ldg(p.bias + c0 + k) : 0.0f;
+// A warp keeps the scales and biases of its tile's N columns (a multiple of 32)
+// in shared memory; they are fetched into registers ahead of their use.
+template <int N>
+struct Scales {
+  float s[N / 32], b[N / 32];
+  __device__ __forceinline__ void fetch(const I8Params& p, int c0) {
+#pragma unroll
+    for (int k = 0; k < N / 32; ++k) {
+      const int c = c0 + 32 * k + (threadIdx.x & 31);
+      const bool in = c < p.cols;
+      s[k] = in ? __ldg(p.w_scale + c) : 0.0f;
+      b[k] = in && p.bias ? __ldg(p.bias + c) : 0.0f;
+    }
   }
-  __syncwarp();
-}
+  __device__ __forceinline__ void stage(float* scales) const {   // then N biases
+    __syncwarp();                                    // the last tile's have been read
+#pragma unroll
+    for (int k = 0; k < N / 32; ++k) {
+      scales[32 * k + (threadIdx.x & 31)] = s[k];
+      scales[N + 32 * k + (threadIdx.x & 31)] = b[k];
+    }
+    __syncwarp();
+  }
+};
 
 __device__ __forceinline__ void store32(void* y, const uint32_t* w) {   // 32 bytes, so aligned
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y), "r"(w[0]), "r"(w[1]),
@@ -627,7 +640,11 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
   int* turn = reinterpret_cast<int*>(gbase + S::TURN + (warp & 3) * TURN_BYTES);
   float* scales = reinterpret_cast<float*>(gbase + S::SCALES) + (warp & 3) * 2 * BN;
   if (warp >= 2) {
-    if (p.split == 1) stage_scales(p, scales, nt * BN, BN);
+    if (p.split == 1) {
+      Scales<BN> columns;
+      columns.fetch(p, nt * BN);
+      columns.stage(scales);
+    }
     bool ok = mbar_wait(ACC, 0, wc, W_EPI_P_FULL);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
@@ -749,8 +766,11 @@ __device__ __forceinline__ void commit_own(uint32_t leader, uint32_t bar) {
       "r"(leader)
       : "memory");
 }
+// Without .release.cluster, which waits for the warp's stores to y (1.8 of 12.9
+// stalled warps at K = 1024): what it hands over are TMEM columns, read to the
+// end and ordered by tcgen05's own fences.
 __device__ __forceinline__ void arrive_peer(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // mbar_wait_warp for arrivals from the other CTA
 __device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity, const WaitCtl& c,
@@ -928,14 +948,28 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
     const uint32_t lane_addr = (static_cast<uint32_t>(q * 32) << 16) + half;
     uint32_t nacc = 0;
     rows_are_coded();
-    for (int unit = first; unit < p.n_units; unit += stride, ++nacc) {
+    // the next tile's place and scales are fetched while this one's sums are
+    // still being formed
+    int64_t row_next = 0;
+    int col_next = 0;
+    float sx_next = 0.0f;
+    Scales<COLS> columns;
+    auto fetch = [&](int unit) {
       int mt, nt;
       pair_unit(p, unit, mt, nt);
+      row_next = static_cast<int64_t>(mt) * 2 * BM + rank * BM + q * 32 + lane;
+      col_next = nt * BN + half;
+      sx_next = row_next < p.rows ? __ldg(p.x_scale + row_next) : 0.0f;
+      columns.fetch(p, col_next);
+    };
+    if (first < p.n_units) fetch(first);
+    for (int unit = first; unit < p.n_units; unit += stride, ++nacc) {
       const int ab = nacc & 1;
-      const int64_t row = static_cast<int64_t>(mt) * 2 * BM + rank * BM + q * 32 + lane;
-      const int col = nt * BN + half;
-      const float sx = row < p.rows ? __ldg(p.x_scale + row) : 0.0f;
-      stage_scales(p, scales, col, COLS);
+      const int64_t row = row_next;
+      const int col = col_next;
+      const float sx = sx_next;
+      columns.stage(scales);
+      if (unit + stride < p.n_units) fetch(unit + stride);
       if (!mbar_wait_warp(ACC_FULL(ab), (nacc >> 1) & 1, wc, W_EPI_P_FULL)) break;
       tc_fence_after();
       float bits[2][32];
