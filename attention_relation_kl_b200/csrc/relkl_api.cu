@@ -862,6 +862,8 @@ relkl_status relkl_adamw(int32_t n_tensors, const relkl_adamw_tensor* tensors,
   p.b2 = static_cast<float>(a.beta2);
   p.c2 = static_cast<float>(1.0 - a.beta2);
   p.eps = static_cast<float>(a.eps);
+  p.rbc2 = static_cast<float>(1.0 / std::sqrt(p.bc2));
+  p.step_size = static_cast<float>(a.lr / p.bc1);
   p.lr_dev = a.lr_dev;
   p.step_dev = reinterpret_cast<const long long*>(a.step_dev);
   p.grad_scale = a.grad_scale;
@@ -912,6 +914,7 @@ relkl_status relkl_adamw(int32_t n_tensors, const relkl_adamw_tensor* tensors,
         g.v_scale = t.v_scale;
         g.n = t.n;
         g.weight_decay = t.weight_decay;
+        g.decay = static_cast<float>(1.0 - a.lr * static_cast<double>(t.weight_decay));
         g.grad_bf16 = gb;
         g.param_bf16 = pb;
         g.wide = aligned(t.grad, gb ? 8 : 16) && aligned(t.param, pb ? 8 : 16) &&

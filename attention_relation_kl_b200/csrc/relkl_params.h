@@ -105,7 +105,8 @@ struct RotaryParams {
 
 // AdamW: tables of tensors travel in the kernel's parameters (32,764 bytes at
 // most); a call with few of them copies a small table.
-constexpr int kAdamwFew = 32;
+constexpr int kAdamwFew = 16;
+constexpr int kAdamwSome = 96;
 constexpr int kAdamwMost = 384;
 
 struct AdamwTensor {
@@ -115,6 +116,7 @@ struct AdamwTensor {
   float *m_scale, *v_scale;  // 8-bit states: one per 256 elements
   int64_t n;
   float weight_decay;
+  float decay;               // 1 - lr weight_decay, of the plan's lr
   uint8_t grad_bf16, param_bf16;
   uint8_t wide;              // every pointer allows accesses of four (eight) elements
 };
@@ -122,6 +124,7 @@ struct AdamwTensor {
 struct AdamwPlan {
   double lr, bc1, bc2, log_b1, log_b2;
   float b1, c1, b2, c2, eps;   // c = 1 - b
+  float rbc2, step_size;       // 1 / sqrt(bc2), lr / bc1
   const float* lr_dev;         // device, or null: lr
   const long long* step_dev;   // device, or null: bc1, bc2
   const float* grad_scale;     // device, or null: 1
