@@ -13,6 +13,7 @@ from .ops import (RelationKL, make_desc, relation_kl, relkl_bwd, relkl_bwd_qkv, 
 from .positions import (Rotary, RotaryFreqs, relkl_rotary, relkl_rotary_qkv, rotary, rotary_freqs)
 from .optim import AdamW, AdamWState, adamw_state, relkl_adamw, relkl_grad_norm
 from .int8 import relkl_linear_i8, relkl_matmul_i8, relkl_quantize_rows
+from .distill import student_step, teacher_relations_i8
 
 __all__ = ["RelationKL", "make_desc", "relation_kl", "relkl_bwd", "relkl_bwd_qkv", "relkl_fwd",
            "relkl_fwd_noalloc", "relkl_fwd_qkv", "relkl_get_device_error", "relkl_path_for",
@@ -20,4 +21,5 @@ __all__ = ["RelationKL", "make_desc", "relation_kl", "relkl_bwd", "relkl_bwd_qkv
            "workspace", "relkl_rope_bwd", "relkl_weight_grad", "student_weight_grads",
            "relkl_cast_bf16", "Rotary", "RotaryFreqs", "relkl_rotary", "relkl_rotary_qkv", "rotary",
            "rotary_freqs", "AdamW", "AdamWState", "adamw_state", "relkl_adamw", "relkl_grad_norm",
-           "relkl_linear_i8", "relkl_matmul_i8", "relkl_quantize_rows"]
+           "relkl_linear_i8", "relkl_matmul_i8", "relkl_quantize_rows",
+           "student_step", "teacher_relations_i8"]

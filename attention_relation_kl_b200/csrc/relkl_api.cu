@@ -358,7 +358,11 @@ bool matrix_ok(const void* x, int32_t dtype, int64_t stride, int32_t K) {
 bool wide_rows(const void* x, int32_t dtype, int64_t stride, int bytes = 16) {
   return aligned(x, bytes) && stride * static_cast<int64_t>(element_size(dtype)) % bytes == 0;
 }
-int64_t code_pitch(int32_t K) { return (static_cast<int64_t>(K) + 15) / 16 * 16; }
+// rows of codes start at 128-byte lines, short ones at 16 bytes
+int64_t code_pitch(int32_t K) {
+  const int64_t line = K >= 128 ? 128 : 16;
+  return (K + line - 1) / line * line;
+}
 bool few_rows(int64_t rows, int32_t K) {
   return rows <= kGemvRows && rows * code_pitch(K) <= kGemvBytes;
 }

@@ -15,6 +15,7 @@
 //     by the weights' bytes, and at these sizes by the launch.
 //   * relkl_gemm_i8_kernel: tcgen05.mma kind::i8 (s8 x s8 -> s32) with both
 //     operands K-major in 128-byte swizzled shared memory, fed by TMA.
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda.h>
@@ -120,6 +121,19 @@ struct Held<__nv_bfloat16> {
   static constexpr int kBits = 16;
   uint4 w;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = __ldcg(reinterpret_cast<const uint4*>(p)); }
+  // from any element: words where they are aligned, else a half, three words
+  // and a half
+  __device__ __forceinline__ void load_any(const __nv_bfloat16* p) {
+    if ((reinterpret_cast<uintptr_t>(p) & 2) == 0) {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+      w = make_uint4(__ldg(q), __ldg(q + 1), __ldg(q + 2), __ldg(q + 3));
+    } else {
+      const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(h + 1);
+      const uint32_t a = __ldg(h), b = __ldg(q), c = __ldg(q + 1), d = __ldg(q + 2), e = __ldg(h + 7);
+      w = make_uint4(a | (b << 16), __funnelshift_l(b, c, 16), __funnelshift_l(c, d, 16), (d >> 16) | (e << 16));
+    }
+  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -136,6 +150,10 @@ struct Held<float> {
   __device__ __forceinline__ void load(const float* p) {
     a = __ldcg(reinterpret_cast<const float4*>(p));
     b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void load_any(const float* p) {
+    a = make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
+    b = make_float4(__ldg(p + 4), __ldg(p + 5), __ldg(p + 6), __ldg(p + 7));
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
@@ -193,8 +211,8 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* part) {
 // eight elements of it: a warp of eight (WARPS), or a block.  The groups stay
 // in registers between the search for the largest and the coding; what a longer
 // row has beyond them is read again (from L2).
-// `wide`: rows start at 16-byte boundaries in both arrays, so groups of eight
-// can move at once.  32K rows of 4096 bf16: 64 us, 6.3 TB/s; with 2 or 8 groups
+// `wide`: rows of x start at 16-byte boundaries, so its groups can move at
+// once.  32K rows of 4096 bf16: 64 us, 6.3 TB/s; with 2 or 8 groups
 // to a thread 94 and 72 us.
 template <typename T, bool WARPS>
 __global__ void __launch_bounds__(512, 2) relkl_quantize_rows_kernel(const RowsParams p) {
@@ -206,18 +224,18 @@ __global__ void __launch_bounds__(512, 2) relkl_quantize_rows_kernel(const RowsP
   const int me = WARPS ? threadIdx.x & 31 : threadIdx.x, step = WARPS ? 32 : blockDim.x;
   const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
   int8_t* q = p.q + row * p.q_stride;
-  const int groups = p.wide ? p.K / 8 : 0;
+  const int groups = p.K / 8;
   Held<T> v[HOLD];
 #pragma unroll
   for (int h = 0; h < HOLD; ++h)
-    if (h * step + me < groups) v[h].load(x + 8 * (h * step + me));
+    if (h * step + me < groups) p.wide ? v[h].load(x + 8 * (h * step + me)) : v[h].load_any(x + 8 * (h * step + me));
   uint32_t most = 0;
 #pragma unroll
   for (int h = 0; h < HOLD; ++h)
     if (h * step + me < groups) most = largest(v[h], most);
   for (int g = HOLD * step + me; g < groups; g += step) {
     Held<T> h;
-    h.load(x + 8 * g);
+    p.wide ? h.load(x + 8 * g) : h.load_any(x + 8 * g);
     most = largest(h, most);
   }
 #pragma unroll 4
@@ -241,7 +259,7 @@ __global__ void __launch_bounds__(512, 2) relkl_quantize_rows_kernel(const RowsP
   }
   for (int g = HOLD * step + me; g < groups; g += step) {
     Held<T> h;
-    h.load(x + 8 * g);
+    p.wide ? h.load(x + 8 * g) : h.load_any(x + 8 * g);
     bool again;
     __stcg(reinterpret_cast<uint2*>(q + 8 * g), coder.codes(h, again));
     if (again)
@@ -279,10 +297,10 @@ __global__ void __launch_bounds__(256) relkl_gemv_i8_kernel(const GemvParams p) 
     if (r >= p.rows) break;
     const T* x = static_cast<const T*>(p.x) + r * p.x_stride;
     uint32_t most = 0;
-    const int groups = p.wide ? p.K / 8 : 0;
+    const int groups = p.K / 8;
     for (int g = threadIdx.x; g < groups; g += 256) {
       Held<T> h;
-      h.load(x + 8 * g);
+      p.wide ? h.load(x + 8 * g) : h.load_any(x + 8 * g);
       most = largest(h, most);
     }
     for (int i = 8 * groups + threadIdx.x; i < p.K; i += 256)
@@ -292,7 +310,7 @@ __global__ void __launch_bounds__(256) relkl_gemv_i8_kernel(const GemvParams p) 
     int8_t* q = codes + r * pitch;
     for (int g = threadIdx.x; g < groups; g += 256) {
       Held<T> h;
-      h.load(x + 8 * g);
+      p.wide ? h.load(x + 8 * g) : h.load_any(x + 8 * g);
       bool again;
       *reinterpret_cast<uint2*>(q + 8 * g) = coder.codes(h, again);
       if (again)
@@ -368,6 +386,7 @@ struct Smem {
   static constexpr int PITCH = BN + 4;
   static_assert(BM * PITCH * 4 <= TURN, "partial sums take the stages' place");
   static_assert(ALLOC <= 232448, "shared memory exceeds 227 KB");
+  static_assert(BN == 64 || BN == 128, "the accumulator takes a power of two of TMEM columns");
 };
 
 // s8 x s8 -> s32, dense, both operands K-major
@@ -723,6 +742,7 @@ struct PairSmem {
   static constexpr int MISC = BARS + (2 * STAGES + 5) * 8;
   static constexpr int ALLOC = MISC + 16 + 1024;
   static_assert(ALLOC <= 232448, "shared memory exceeds 227 KB");
+  static_assert(BN == 128 || BN == 256, "two accumulators take a power of two of TMEM columns");
 };
 
 // a load into this CTA's shared memory that signals the barrier `bar` of the
@@ -1107,16 +1127,34 @@ cudaError_t gemm_pair(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
   return launch_cluster(kernel, p, 2 * pairs, i8::PAIR_THREADS, 2, S::ALLOC, c.after_rows, stream);
 }
 
+// Four kernels by the width of their tiles, the one with the least estimated
+// time: waves of tiles times the time of one wave, as measured relative to one
+// another (K = 4096, full waves: 9.3, 11.5, 10.0 and 13.8 us; K = 512: 4.4, 5.2,
+// 5.9 and 7.6 us).  So 128 rows x 4096 channels take 64 columns a tile (10.6
+// us; the others 11.3, 12.0, 15.4), 500 rows pairs with 128 columns (12.6; 64
+// columns 20.4, pairs with 256 16.0), 1000 rows pairs with 256 (16.9; 38.3,
+// 23.1, 21.2).  Where tiles of 64 columns leave SMs idle, K is split over up to
+// four of them: 16 rows x 1024 channels 9.8 us alone, 8.8 and 6.9 us with two
+// and four shares, 11.0 us with eight.
 template <typename U>
 cudaError_t gemm_pick(I8Params& p, const I8Call& c, int num_sms, cudaStream_t stream) {
-  const int64_t m = (p.rows + i8::BM - 1) / i8::BM;
   p.k_chunks = (c.K + i8::BK - 1) / i8::BK;
-  auto tiles = [&](int bn) { return m * ((p.cols + bn - 1) / bn); };
   p.split = 1;
-  if (tiles(256) >= num_sms) return gemm_pair<256, U>(p, c, num_sms, stream);
-  if (tiles(128) >= num_sms) return gemm<128, U>(p, c, stream);
-  while (p.split < 8 && tiles(64) * p.split * 2 <= num_sms && p.k_chunks >= p.split * 8) p.split *= 2;
-  return gemm<64, U>(p, c, stream);
+  auto tiles = [&](int bm, int bn) { return (p.rows + bm - 1) / bm * ((p.cols + bn - 1) / bn); };
+  auto cost = [&](int64_t n, int at_once, int wave) { return (n + at_once - 1) / at_once * wave; };
+  const int pairs = num_sms / 2;
+  const int64_t t64 = tiles(i8::BM, 64);
+  const int64_t one64 = cost(t64, num_sms, 93), one128 = cost(tiles(i8::BM, 128), num_sms, 115);
+  const int64_t two128 = cost(tiles(2 * i8::BM, 128), pairs, 100);
+  const int64_t two256 = cost(tiles(2 * i8::BM, 256), pairs, 138);
+  const int64_t least = std::min(std::min(one64, one128), std::min(two128, two256));
+  if (two256 == least) return gemm_pair<256, U>(p, c, num_sms, stream);
+  if (one64 == least) {
+    while (p.split < 4 && t64 * p.split * 2 <= num_sms && p.k_chunks >= p.split * 8) p.split *= 2;
+    return gemm<64, U>(p, c, stream);
+  }
+  if (two128 == least) return gemm_pair<128, U>(p, c, num_sms, stream);
+  return gemm<128, U>(p, c, stream);
 }
 
 }  // namespace

@@ -103,7 +103,8 @@ def relkl_quantize_rows(x: torch.Tensor, *, stream=None) -> Tuple[torch.Tensor, 
     if x.dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {x.dtype}")
     rows, K, stride = _matrix(x, "x")
-    pitch = (K + 15) // 16 * 16
+    line = 128 if K >= 128 else 16
+    pitch = (K + line - 1) // line * line
     with _on(x.device, stream) as handle:
         q = torch.empty(rows, pitch, dtype=torch.int8, device=x.device)
         scale = torch.empty(rows, dtype=torch.float32, device=x.device)

@@ -452,17 +452,30 @@ def relkl_weight_grad(h: torch.Tensor, dx_pre: torch.Tensor, *, out: Optional[to
 
 def student_weight_grads(pairs: Dict[str, Tuple[torch.Tensor, torch.Tensor]], h_s: torch.Tensor,
                          rope_base: float, pos_scale: float, causal: bool = True,
-                         dkl: Optional[Dict[str, torch.Tensor]] = None) -> Dict[str, torch.Tensor]:
+                         dkl: Optional[Dict[str, torch.Tensor]] = None, *, freqs=None,
+                         positions: Optional[torch.Tensor] = None,
+                         interleaved: bool = False) -> Dict[str, torch.Tensor]:
     """dW_q, dW_k, dW_v of the student: relation-KL forward and backward over the
     relations given ({rel: (x_t, x_s)}, one fused launch each), RoPE backward for q
-    and k at the student's positions, and the weight gradient against h_s [B, N, D]."""
+    and k at the student's positions, and the weight gradient against h_s [B, N, D].
+
+    With ``freqs`` (rotary_freqs) the students' q and k were rotated by them instead of
+    by the powers of ``rope_base``, at ``pos_scale`` times the token numbers or the given
+    ``positions``, and are turned back by relkl_rotary_qkv, all relations in one launch."""
     rels = list(pairs)
     outs = relkl_fwd_qkv([pairs[r] for r in rels], causal)
     dxs = relkl_bwd_qkv([pairs[r] for r in rels], [o[1] for o in outs],
                         None if dkl is None else [dkl.get(r) for r in rels], causal)
-    grads = {}
-    for r, dx in zip(rels, dxs):
-        pre = relkl_rope_bwd(dx, rope_base, pos_scale, 0.0, apply=(r != "v"))
-        grads[r] = relkl_weight_grad(h_s, pre)
-    return grads
-
+    if freqs is None:
+        if positions is not None or interleaved:
+            raise ValueError("positions and interleaved need freqs")
+        pres = [relkl_rope_bwd(dx, rope_base, pos_scale, 0.0, apply=(r != "v"))
+                for r, dx in zip(rels, dxs)]
+    else:
+        from .positions import relkl_rotary_qkv
+        pres = [torch.empty((dx.shape[0], dx.shape[2], dx.shape[1], dx.shape[3]),
+                            dtype=torch.bfloat16, device=dx.device) for dx in dxs]
+        relkl_rotary_qkv(dxs, freqs.inv_freq, apply=[r != "v" for r in rels], pos_scale=pos_scale,
+                         positions=positions, mscale=freqs.mscale, interleaved=interleaved,
+                         inverse=True, out=[p.transpose(1, 2) for p in pres])
+    return {r: relkl_weight_grad(h_s, pre) for r, pre in zip(rels, pres)}
