@@ -493,49 +493,38 @@ __device__ __forceinline__ void store32(void* y, const uint32_t* w) {   // 32 by
                : "memory");
 }
 
-// A warp's 32 rows x 32 columns, one row to a lane.  Where rows of y start at
-// 32-byte boundaries (y_wide 2) each lane stores whole sectors of its row, at
-// 16-byte boundaries (1) halves of them.  Else the sums are turned through
-// shared memory, and the warp stores one row at a time, a column to a lane.
+// A lane's 32 sums of one row, scaled and rounded, as words of y.
 template <typename U>
-__device__ __forceinline__ void store_block(const I8Params& p, int* turn, const float* scales,
-                                            const float* biases, int64_t row, int c0, float sx,
-                                            const float (&bits)[32]) {
-  const int lane = threadIdx.x & 31;
-  if (p.y_wide && c0 + 32 <= p.cols) {
-    constexpr int W = 32 * sizeof(U) / 4;             // words of the block's row
-    uint32_t w[W];
+__device__ __forceinline__ void scaled_words(const float* scales, const float* biases, float sx,
+                                             const float (&bits)[32], uint32_t (&w)[8 * sizeof(U)]) {
 #pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-      const float4 s = *reinterpret_cast<const float4*>(scales + k);
-      const float4 b = *reinterpret_cast<const float4*>(biases + k);
-      const float v0 = fmaf(static_cast<float>(__float_as_int(bits[k])), sx * s.x, b.x);
-      const float v1 = fmaf(static_cast<float>(__float_as_int(bits[k + 1])), sx * s.y, b.y);
-      const float v2 = fmaf(static_cast<float>(__float_as_int(bits[k + 2])), sx * s.z, b.z);
-      const float v3 = fmaf(static_cast<float>(__float_as_int(bits[k + 3])), sx * s.w, b.w);
-      if constexpr (sizeof(U) == 4) {
-        w[k] = __float_as_uint(v0);
-        w[k + 1] = __float_as_uint(v1);
-        w[k + 2] = __float_as_uint(v2);
-        w[k + 3] = __float_as_uint(v3);
-      } else {
-        w[k / 2] = pack_bf16x2(v0, v1);
-        w[k / 2 + 1] = pack_bf16x2(v2, v3);
-      }
+  for (int k = 0; k < 32; k += 4) {
+    const float4 s = *reinterpret_cast<const float4*>(scales + k);
+    const float4 b = *reinterpret_cast<const float4*>(biases + k);
+    const float v0 = fmaf(static_cast<float>(__float_as_int(bits[k])), sx * s.x, b.x);
+    const float v1 = fmaf(static_cast<float>(__float_as_int(bits[k + 1])), sx * s.y, b.y);
+    const float v2 = fmaf(static_cast<float>(__float_as_int(bits[k + 2])), sx * s.z, b.z);
+    const float v3 = fmaf(static_cast<float>(__float_as_int(bits[k + 3])), sx * s.w, b.w);
+    if constexpr (sizeof(U) == 4) {
+      w[k] = __float_as_uint(v0);
+      w[k + 1] = __float_as_uint(v1);
+      w[k + 2] = __float_as_uint(v2);
+      w[k + 3] = __float_as_uint(v3);
+    } else {
+      w[k / 2] = pack_bf16x2(v0, v1);
+      w[k / 2 + 1] = pack_bf16x2(v2, v3);
     }
-    if (row < p.rows) {
-      uint32_t* y = reinterpret_cast<uint32_t*>(static_cast<U*>(p.y) + row * p.y_stride + c0);
-      if (p.y_wide == 2) {
-#pragma unroll
-        for (int k = 0; k < W; k += 8) store32(y + k, w + k);
-      } else {
-#pragma unroll
-        for (int k = 0; k < W; k += 4)
-          *reinterpret_cast<uint4*>(y + k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
-      }
-    }
-    return;
   }
+}
+
+// A warp's 32 rows x 32 columns where rows of y start anywhere: the sums are
+// turned through shared memory, and the warp stores one row at a time, a
+// column to a lane.
+template <typename U>
+__device__ __forceinline__ void store_turned(const I8Params& p, int* turn, const float* scales,
+                                             const float* biases, int64_t row, int c0, float sx,
+                                             const float (&bits)[32]) {
+  const int lane = threadIdx.x & 31;
   __syncwarp();                                      // the last block has been read
 #pragma unroll
   for (int k = 0; k < 32; ++k) turn[lane * TURN_PITCH + k] = __float_as_int(bits[k]);
@@ -549,6 +538,32 @@ __device__ __forceinline__ void store_block(const I8Params& p, int* turn, const 
     const float s = __shfl_sync(0xffffffffu, sx, r);
     const float v = fmaf(static_cast<float>(turn[r * TURN_PITCH + lane]), s * sw, b);
     if (r < left && c0 + lane < p.cols) y[r * p.y_stride] = from_float<U>(v);
+  }
+}
+
+// A warp's 32 rows x 32 columns, one row to a lane.  Where rows of y start at
+// 32-byte boundaries (y_wide 2) each lane stores whole sectors of its row, at
+// 16-byte boundaries (1) halves of them; else as above.
+template <typename U>
+__device__ __forceinline__ void store_block(const I8Params& p, int* turn, const float* scales,
+                                            const float* biases, int64_t row, int c0, float sx,
+                                            const float (&bits)[32]) {
+  if (!p.y_wide || c0 + 32 > p.cols) {
+    store_turned<U>(p, turn, scales, biases, row, c0, sx, bits);
+    return;
+  }
+  constexpr int W = 8 * sizeof(U);                   // words of the block's row
+  uint32_t w[W];
+  scaled_words<U>(scales, biases, sx, bits, w);
+  if (row >= p.rows) return;
+  uint32_t* y = reinterpret_cast<uint32_t*>(static_cast<U*>(p.y) + row * p.y_stride + c0);
+  if (p.y_wide == 2) {
+#pragma unroll
+    for (int k = 0; k < W; k += 8) store32(y + k, w + k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < W; k += 4)
+      *reinterpret_cast<uint4*>(y + k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
   }
 }
 
@@ -736,12 +751,14 @@ struct PairSmem {
   static constexpr int A_BYTES = BM * BK, B_BYTES = BN / 2 * BK;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = 5;
-  static constexpr int TURN = STAGES * STAGE;
-  static constexpr int SCALES = TURN + PAIR_EPI * TURN_BYTES;
+  static constexpr int OUT = STAGES * STAGE;           // epilogue warps' boxes of y, or turned blocks
+  static constexpr int OUT_BYTES = 5120;
+  static constexpr int SCALES = OUT + PAIR_EPI * OUT_BYTES;
   static constexpr int BARS = SCALES + PAIR_EPI * BN * 4;   // full, empty, acc_full[2], acc_empty[2], drain
   static constexpr int MISC = BARS + (2 * STAGES + 5) * 8;
   static constexpr int ALLOC = MISC + 16 + 1024;
   static_assert(ALLOC <= 232448, "shared memory exceeds 227 KB");
+  static_assert(OUT % 1024 == 0 && OUT_BYTES % 1024 == 0 && OUT_BYTES >= TURN_BYTES, "swizzled boxes");
   static_assert(BN == 128 || BN == 256, "two accumulators take a power of two of TMEM columns");
 };
 
@@ -961,7 +978,8 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
     __syncwarp();
   } else {
     const int q = warp & 3, epi = warp - 2;
-    int* turn = reinterpret_cast<int*>(gbase + S::TURN + epi * TURN_BYTES);
+    const uint32_t box = base + S::OUT + epi * S::OUT_BYTES;
+    int* turn = reinterpret_cast<int*>(gbase + S::OUT + epi * S::OUT_BYTES);
     float* scales = reinterpret_cast<float*>(gbase + S::SCALES) + epi * BN;   // and biases
     constexpr int COLS = BN / 2;
     const int half = (epi >> 2) * COLS;
@@ -1005,10 +1023,38 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
           __syncwarp();
           if (lane == 0) arrive_peer(peer(ACC_EMPTY(ab), 0));
         }
-        if (col + 32 * k < p.cols)
-          store_block<U>(p, turn, scales + 32 * k, scales + COLS + 32 * k, row, col + 32 * k, sx, bits[k & 1]);
+        const int c = col + 32 * k;
+        if (!p.y_wide) {
+          if (c < p.cols) store_turned<U>(p, turn, scales + 32 * k, scales + COLS + 32 * k, row, c, sx, bits[k & 1]);
+          continue;
+        }
+        // boxes of 32 rows x 128 bytes, swizzled against bank conflicts, go to
+        // y by TMA: whole lines, and what lies past the edges is left out
+        constexpr int W = 8 * sizeof(U), PER = 128 / (4 * W);   // words of a block's row; blocks of a box
+        const int part = k % PER;
+        if (part == 0) {
+          if (lane == 0) bulk_wait_read<0>();                   // the last box has been read
+          __syncwarp();
+        }
+        uint32_t w[W];
+        scaled_words<U>(scales + 32 * k, scales + COLS + 32 * k, sx, bits[k & 1], w);
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j)
+          st_shared_v4(box + lane * 128 + (((part * (W / 4) + j) ^ (lane & 7)) << 4), w[4 * j], w[4 * j + 1],
+                       w[4 * j + 2], w[4 * j + 3]);
+        if (part == PER - 1) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int c_box = c - 32 * (PER - 1);
+          const int64_t r_box = row - lane;
+          if (lane == 0) {
+            if (c_box < p.cols && r_box < p.rows) tma_store_2d(&p.tm_y, box, c_box, static_cast<int>(r_box));
+            bulk_commit();
+          }
+        }
       }
     }
+    if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
 
@@ -1074,6 +1120,17 @@ bool encode_codes(CUtensorMap* m, const int8_t* q, int64_t rows, int K, int64_t 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// y as boxes of 32 rows x 128 bytes
+template <typename U>
+bool encode_out(CUtensorMap* m, const I8Params& p, EncodeTiled encode) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.cols), static_cast<cuuint64_t>(p.rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.y_stride) * sizeof(U)};
+  const cuuint32_t boxes[2] = {128 / sizeof(U), 32}, ones[2] = {1, 1};
+  return encode(m, sizeof(U) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.y,
+                dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename K>
 cudaError_t launch_cluster(K kernel, const I8Params& p, unsigned grid, int threads, int cluster,
                            int smem, bool ahead, cudaStream_t stream) {
@@ -1114,7 +1171,8 @@ cudaError_t gemm_pair(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
   using S = i8::PairSmem<BN>;
   const int64_t m = (p.rows + 2 * i8::BM - 1) / (2 * i8::BM), n = (p.cols + BN - 1) / BN;
   if (!encode_codes(&p.tm_a, c.q, p.rows, c.K, c.q_stride, i8::BM, c.encode) ||
-      !encode_codes(&p.tm_b, c.w, p.cols, c.K, c.w_stride, BN / 2, c.encode))
+      !encode_codes(&p.tm_b, c.w, p.cols, c.K, c.w_stride, BN / 2, c.encode) ||
+      (p.y_wide && !encode_out<U>(&p.tm_y, p, c.encode)))
     return cudaErrorInvalidValue;
   if (m * n + num_sms > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   p.m_tiles = static_cast<int>(m);

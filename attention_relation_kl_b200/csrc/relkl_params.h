@@ -183,6 +183,7 @@ struct GemvParams {
 struct I8Params {
   CUtensorMap tm_a;                   // codes [rows, K]: box 128 bytes x 128 rows, 128B swizzle
   CUtensorMap tm_b;                   // weights [cols, K]: box 128 bytes x BN rows
+  CUtensorMap tm_y;                   // y: box 128 bytes x 32 rows, 128B swizzle (pairs, y_wide)
   const float *x_scale, *w_scale, *bias;
   void* y;
   int64_t rows, y_stride;
