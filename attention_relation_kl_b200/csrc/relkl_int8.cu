@@ -517,44 +517,55 @@ __device__ __forceinline__ void scaled_words(const float* scales, const float* b
   }
 }
 
-// A warp's 32 rows x 32 columns where rows of y start anywhere: the sums are
-// turned through shared memory, and the warp stores one row at a time, a
-// column to a lane.
-template <typename U>
-__device__ __forceinline__ void store_turned(const I8Params& p, int* turn, const float* scales,
-                                             const float* biases, int64_t row, int c0, float sx,
-                                             const float (&bits)[32]) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();                                      // the last block has been read
-#pragma unroll
-  for (int k = 0; k < 32; ++k) turn[lane * TURN_PITCH + k] = __float_as_int(bits[k]);
+// Rows of y may start anywhere: then a warp turns its 32 rows through shared
+// memory and stores along them, WORDS words of a row to as many lanes.  In
+// bf16 a word is two columns; a row that starts in the middle of a word has
+// them paired with one column's shift.
+template <typename U, int WORDS>
+__device__ __forceinline__ void store_turned(const I8Params& p, const uint32_t* turn, int64_t row0, int c0) {
+  const int lane = threadIdx.x & 31, l = lane % WORDS;
+  const int left = p.cols - c0;
   __syncwarp();
-  const float sw = scales[lane], b = biases[lane];
-  const int64_t row0 = row - lane;
-  U* y = static_cast<U*>(p.y) + row0 * p.y_stride + c0 + lane;
-  const int64_t left = p.rows - row0;
 #pragma unroll 8
-  for (int r = 0; r < 32; ++r) {
-    const float s = __shfl_sync(0xffffffffu, sx, r);
-    const float v = fmaf(static_cast<float>(turn[r * TURN_PITCH + lane]), s * sw, b);
-    if (r < left && c0 + lane < p.cols) y[r * p.y_stride] = from_float<U>(v);
+  for (int r = lane / WORDS; r < 32; r += 32 / WORDS) {
+    if (row0 + r >= p.rows) break;
+    U* y = static_cast<U*>(p.y) + (row0 + r) * p.y_stride + c0;
+    const uint32_t a = turn[r * TURN_PITCH + l];
+    if constexpr (sizeof(U) == 4) {
+      if (l < left) y[l] = __uint_as_float(a);
+    } else {
+      const uint32_t b = turn[r * TURN_PITCH + min(l + 1, WORDS - 1)];
+      unsigned short* h = reinterpret_cast<unsigned short*>(y);
+      const int shift = (reinterpret_cast<uintptr_t>(y) & 2) != 0;   // the same for the row's lanes
+      const uint32_t pair = shift ? (a >> 16) | (b << 16) : a;
+      const int c = 2 * l + shift;
+      if (c + 1 < left && c + 1 < 2 * WORDS)
+        *reinterpret_cast<uint32_t*>(h + c) = pair;
+      else if (c < left)
+        h[c] = static_cast<unsigned short>(pair);
+      if (shift && l == 0) h[0] = static_cast<unsigned short>(a);
+    }
   }
+  __syncwarp();     // read before the next block is written
 }
 
 // A warp's 32 rows x 32 columns, one row to a lane.  Where rows of y start at
 // 32-byte boundaries (y_wide 2) each lane stores whole sectors of its row, at
 // 16-byte boundaries (1) halves of them; else as above.
 template <typename U>
-__device__ __forceinline__ void store_block(const I8Params& p, int* turn, const float* scales,
+__device__ __forceinline__ void store_block(const I8Params& p, uint32_t* turn, const float* scales,
                                             const float* biases, int64_t row, int c0, float sx,
                                             const float (&bits)[32]) {
-  if (!p.y_wide || c0 + 32 > p.cols) {
-    store_turned<U>(p, turn, scales, biases, row, c0, sx, bits);
-    return;
-  }
   constexpr int W = 8 * sizeof(U);                   // words of the block's row
   uint32_t w[W];
   scaled_words<U>(scales, biases, sx, bits, w);
+  if (!p.y_wide || c0 + 32 > p.cols) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < W; ++k) turn[lane * TURN_PITCH + k] = w[k];
+    store_turned<U, W>(p, turn, row - lane, c0);
+    return;
+  }
   if (row >= p.rows) return;
   uint32_t* y = reinterpret_cast<uint32_t*>(static_cast<U*>(p.y) + row * p.y_stride + c0);
   if (p.y_wide == 2) {
@@ -671,7 +682,7 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
   const bool live = warp >= 2 && row < p.rows;
   if (warp >= 2) rows_are_coded();
   const float sx = live ? p.x_scale[row] : 0.0f;
-  int* turn = reinterpret_cast<int*>(gbase + S::TURN + (warp & 3) * TURN_BYTES);
+  uint32_t* turn = reinterpret_cast<uint32_t*>(gbase + S::TURN + (warp & 3) * TURN_BYTES);
   float* scales = reinterpret_cast<float*>(gbase + S::SCALES) + (warp & 3) * 2 * BN;
   if (warp >= 2) {
     if (p.split == 1) {
@@ -979,7 +990,7 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
   } else {
     const int q = warp & 3, epi = warp - 2;
     const uint32_t box = base + S::OUT + epi * S::OUT_BYTES;
-    int* turn = reinterpret_cast<int*>(gbase + S::OUT + epi * S::OUT_BYTES);
+    uint32_t* turn = reinterpret_cast<uint32_t*>(gbase + S::OUT + epi * S::OUT_BYTES);
     float* scales = reinterpret_cast<float*>(gbase + S::SCALES) + epi * BN;   // and biases
     constexpr int COLS = BN / 2;
     const int half = (epi >> 2) * COLS;
@@ -1024,20 +1035,22 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
           if (lane == 0) arrive_peer(peer(ACC_EMPTY(ab), 0));
         }
         const int c = col + 32 * k;
+        constexpr int W = 8 * sizeof(U), PER = 128 / (4 * W);   // words of a block's row; blocks of 128 bytes
+        const int part = k % PER, c_box = c - 32 * part;
+        uint32_t w[W];
+        scaled_words<U>(scales + 32 * k, scales + COLS + 32 * k, sx, bits[k & 1], w);
         if (!p.y_wide) {
-          if (c < p.cols) store_turned<U>(p, turn, scales + 32 * k, scales + COLS + 32 * k, row, c, sx, bits[k & 1]);
+#pragma unroll
+          for (int j = 0; j < W; ++j) turn[lane * TURN_PITCH + part * W + j] = w[j];
+          if (part == PER - 1 && c_box < p.cols) store_turned<U, 32>(p, turn, row - lane, c_box);
           continue;
         }
         // boxes of 32 rows x 128 bytes, swizzled against bank conflicts, go to
         // y by TMA: whole lines, and what lies past the edges is left out
-        constexpr int W = 8 * sizeof(U), PER = 128 / (4 * W);   // words of a block's row; blocks of a box
-        const int part = k % PER;
         if (part == 0) {
           if (lane == 0) bulk_wait_read<0>();                   // the last box has been read
           __syncwarp();
         }
-        uint32_t w[W];
-        scaled_words<U>(scales + 32 * k, scales + COLS + 32 * k, sx, bits[k & 1], w);
 #pragma unroll
         for (int j = 0; j < W / 4; ++j)
           st_shared_v4(box + lane * 128 + (((part * (W / 4) + j) ^ (lane & 7)) << 4), w[4 * j], w[4 * j + 1],
@@ -1045,7 +1058,6 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
         if (part == PER - 1) {
           fence_proxy_async_smem();
           __syncwarp();
-          const int c_box = c - 32 * (PER - 1);
           const int64_t r_box = row - lane;
           if (lane == 0) {
             if (c_box < p.cols && r_box < p.rows) tma_store_2d(&p.tm_y, box, c_box, static_cast<int>(r_box));
