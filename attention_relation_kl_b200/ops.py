@@ -86,6 +86,11 @@ def _stream(device: torch.device, stream=None) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+# the handle of a device's current stream, without a Stream object where torch has the call
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _on:
     """Makes ``device`` current, and ``stream`` (a torch stream or a cudaStream_t
     handle) if one is given, so that what a call allocates for itself belongs to
@@ -97,7 +102,7 @@ class _on:
     def __enter__(self) -> int:
         index = self.device.index
         if self.stream is None and torch.cuda.current_device() == index:
-            return torch.cuda.current_stream(index).cuda_stream
+            return _current_stream(index)
         self.inner = contextlib.ExitStack()
         self.inner.enter_context(torch.cuda.device(self.device))
         if self.stream is not None:
@@ -105,7 +110,7 @@ class _on:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=self.device)
             self.inner.enter_context(torch.cuda.stream(stream))
-        return torch.cuda.current_stream(index).cuda_stream
+        return _current_stream(index)
 
     def __exit__(self, *exc) -> None:
         if self.inner is not None:

@@ -8,8 +8,8 @@ from __future__ import annotations
 
 import math
 import struct
-from itertools import repeat
-from operator import attrgetter
+from itertools import chain, repeat
+from operator import attrgetter, is_
 from typing import List, NamedTuple, Optional, Sequence, Union
 
 import torch
@@ -22,8 +22,9 @@ __all__ = ["AdamWState", "adamw_state", "relkl_adamw", "relkl_grad_norm", "AdamW
 
 BLOCK = 256     # elements that share one scale of an 8-bit state
 _E4M3 = torch.float8_e4m3fn
-# the layouts of the structs in include/relkl.h
-_TENSOR = struct.Struct("@7Pqiifi")
+# The layouts of the structs in include/relkl.h.  A relkl_adamw_tensor is packed as ten words:
+# seven pointers, the size, the two types, and the weight decay with the reserved zero.
+_TENSOR_WORDS = 10
 _PLAN = struct.Struct("@iiddddqPPP")
 _NORM = struct.Struct("@Pqii")
 
@@ -56,12 +57,22 @@ def adamw_state(param: torch.Tensor, bits: int = 32) -> AdamWState:
                         for _ in range(2)))
 
 
-def _same_device(index: int, *lists: Sequence[torch.Tensor]) -> None:
-    for ts in lists:
-        if set(map(_device, ts)) - {index}:
-            raise ValueError("all tensors must be CUDA tensors on one device (there is no CPU path)")
-        if not all(map(torch.Tensor.is_contiguous, ts)):
-            raise ValueError("tensors must be contiguous")
+def _same_device(index: int, ts: Sequence[torch.Tensor]) -> None:
+    if set(map(_device, ts)) - {index}:
+        raise ValueError("all tensors must be CUDA tensors on one device (there is no CPU path)")
+    if not all(map(torch.Tensor.is_contiguous, ts)):
+        raise ValueError("tensors must be contiguous")
+
+
+def _decay_word(x: float) -> int:
+    return struct.unpack("=q", struct.pack("=fi", x, 0))[0]
+
+
+def _table(grads, params, copies, m, v, m_scale, v_scale, sizes, grad_types, param_types, decay) -> bytes:
+    """relkl_adamw_tensor records; the pointers and types as integers."""
+    types = [g | (p << 32) for g, p in zip(grad_types, param_types)]
+    words = chain.from_iterable(zip(grads, params, copies, m, v, m_scale, v_scale, sizes, types, decay))
+    return struct.pack(f"={_TENSOR_WORDS * len(sizes)}q", *words)
 
 
 def _types(ts: Sequence[torch.Tensor], what: str) -> List[int]:
@@ -95,7 +106,7 @@ def relkl_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     n = len(params)
     if len(grads) != n or len(states) != n or (copies is not None and len(copies) != n):
         raise ValueError("params, grads, states and copies need one entry for each tensor")
-    decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
+    decay = [weight_decay] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
     if len(decay) != n:
         raise ValueError("weight_decay needs one number, or one for each tensor")
     if n == 0:
@@ -118,25 +129,26 @@ def relkl_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         raise TypeError("m and v must both be float32, or both float8_e4m3fn")
     bits = 32 if kinds[0] == torch.float32 else 8
     shapes = list(map(_shape, params))
+    every = [*params]
     for xs in (grads, m, v) if copies is None else (grads, m, v, copies):
         if list(map(_shape, xs)) != shapes:
             raise ValueError("a parameter's gradient, states and copy must have its shape")
-        _same_device(index, xs)
-    _same_device(index, params)
+        every += xs
     sizes = list(map(_numel, params))
     if bits == 8:
+        scales = m_scale + v_scale
+        if any(map(is_, scales, repeat(None))):
+            raise ValueError("8-bit states need their scales")
         blocks = [-(-k // BLOCK) for k in sizes]
-        for xs in (m_scale, v_scale):
-            if any(x is None for x in xs):
-                raise ValueError("8-bit states need their scales")
-            if set(map(_dtype, xs)) != {torch.float32} or list(map(_numel, xs)) != blocks:
-                raise ValueError("8-bit states need a float32 scale for each 256 elements")
-            _same_device(index, xs)
+        if set(map(_dtype, scales)) != {torch.float32} or list(map(_numel, scales)) != blocks + blocks:
+            raise ValueError("8-bit states need a float32 scale for each 256 elements")
+        every += scales
         m_scale, v_scale = map(_ptr, m_scale), map(_ptr, v_scale)
     else:
-        if any(x is not None for x in m_scale + v_scale):
+        if not all(map(is_, m_scale + v_scale, repeat(None))):
             raise ValueError("float32 states have no scales")
         m_scale = v_scale = repeat(0)
+    _same_device(index, every)
     if copies is not None and set(map(_dtype, copies)) != {torch.bfloat16}:
         raise TypeError("copies must be bfloat16")
     lr_ptr = step_ptr = scale_ptr = 0
@@ -146,15 +158,20 @@ def relkl_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         step, step_ptr = 1, _scalar(step, torch.int64, index, "step")
     if grad_scale is not None:
         scale_ptr = _scalar(grad_scale, torch.float32, index, "grad_scale")
-    table = b"".join(map(_TENSOR.pack, map(_ptr, grads), map(_ptr, params),
-                         repeat(0) if copies is None else map(_ptr, copies), map(_ptr, m),
-                         map(_ptr, v), m_scale, v_scale, sizes, _types(grads, "gradients"),
-                         _types(params, "parameters"), decay, repeat(0)))
+    if isinstance(weight_decay, (int, float)):
+        decay = repeat(_decay_word(weight_decay))
+    else:
+        decay = map(_decay_word, decay)
+    table = _table(map(_ptr, grads), map(_ptr, params),
+                   repeat(0) if copies is None else map(_ptr, copies), map(_ptr, m), map(_ptr, v),
+                   m_scale, v_scale, sizes, _types(grads, "gradients"), _types(params, "parameters"),
+                   decay)
     plan = _PLAN.pack(bits, 0, lr, betas[0], betas[1], eps, step, lr_ptr, step_ptr, scale_ptr)
     with _on(params[0].device, stream) as handle:
         check(_abi.lib().relkl_adamw(n, table, plan, handle), "relkl_adamw")
     # what autograd saved of the old values is no longer valid
-    torch.autograd.graph.increment_version(params if copies is None else [*params, *copies])
+    written = params if copies is None else [*params, *copies]
+    torch.autograd.graph.increment_version([x for x in written if not x.is_inference()])
 
 
 def relkl_grad_norm(grads: Sequence[torch.Tensor], max_norm: float = math.inf, *,

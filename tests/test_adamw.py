@@ -98,11 +98,15 @@ def test_norm_refusals():
 
 
 def test_binding_packs_the_structs():
-    assert optim._TENSOR.size == ctypes.sizeof(_abi.relkl_adamw_tensor)
     assert optim._PLAN.size == ctypes.sizeof(_abi.relkl_adamw_plan)
     assert optim._NORM.size == ctypes.sizeof(_abi.relkl_norm_tensor)
-    t = _abi.relkl_adamw_tensor.from_buffer_copy(optim._TENSOR.pack(*range(1, 11), 0.5, 12))
-    assert (t.grad, t.v_scale, t.n, t.param_dtype, t.weight_decay, t.reserved) == (1, 7, 8, 10, 0.5, 12)
+    table = optim._table([1, 11], [2, 12], [3, 13], [4, 14], [5, 15], [6, 16], [7, 17], [8, 18], [0, 1], [1, 0],
+                         [optim._decay_word(0.5), optim._decay_word(0.25)])
+    a, b = (_abi.relkl_adamw_tensor * 2).from_buffer_copy(table)
+    assert len(table) == ctypes.sizeof(_abi.relkl_adamw_tensor) * 2
+    assert (a.grad, a.param, a.copy, a.m, a.v, a.m_scale, a.v_scale, a.n) == (1, 2, 3, 4, 5, 6, 7, 8)
+    assert (a.grad_dtype, a.param_dtype, a.weight_decay, a.reserved) == (0, 1, 0.5, 0)
+    assert (b.v_scale, b.n, b.grad_dtype, b.param_dtype, b.weight_decay) == (17, 18, 1, 0, 0.25)
     p = _abi.relkl_adamw_plan.from_buffer_copy(optim._PLAN.pack(8, 0, 1.0, 2.0, 3.0, 4.0, 5, 6, 7, 8))
     assert (p.lr, p.eps, p.step, p.lr_dev, p.grad_scale) == (1.0, 4.0, 5, 6, 8)
 
