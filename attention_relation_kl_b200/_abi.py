@@ -167,6 +167,22 @@ def lib():
     return _LIB
 
 
+_MARSHAL = None
+
+
+def marshal():
+    """The marshalling module.  Raises if it has not been built."""
+    global _MARSHAL
+    if _MARSHAL is None:
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise ImportError("the marshalling module is missing or was built for another torch; build it "
+                              f"with `python -m attention_relation_kl_b200.build` ({e})") from e
+        _MARSHAL = _marshal
+    return _MARSHAL
+
+
 class RelklError(RuntimeError):
     def __init__(self, code: int, where: str):
         msg = lib().relkl_status_string(code).decode()

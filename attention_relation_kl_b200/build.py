@@ -1,4 +1,5 @@
-"""Build librelkl.so in-tree for sm_100a (B200) with nvcc.
+"""Build librelkl.so in-tree for sm_100a (B200) with nvcc, and the binding's
+marshalling module (plain C++ against torch's headers).
 
     python -m attention_relation_kl_b200.build        # or build() from Python
 
@@ -7,10 +8,12 @@ tree.  nvcc cross-compiles without a GPU.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -19,6 +22,8 @@ LIB = os.path.join(HERE, "librelkl.so")
 SOURCES = ["relkl_api.cu", "relkl_tc.cu", "relkl_simt.cu", "relkl_chain.cu", "relkl_gemm.cu",
            "relkl_rotary.cu", "relkl_adamw.cu", "relkl_int8.cu"]
 HEADERS = ["relkl_device.cuh", "relkl_params.h"]
+MARSHAL_SOURCE = os.path.join(CSRC, "relkl_marshal.cpp")
+MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -45,6 +50,31 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _run(cmd, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Compile the marshalling module if its sources are newer; returns its path."""
+    deps = [MARSHAL_SOURCE, os.path.join(ROOT, "include", "relkl.h"), __file__]
+    if not force and os.path.exists(MARSHAL) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
+        return MARSHAL
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    tmp = MARSHAL + ".tmp"
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", inc,
+          "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+          "-I", sysconfig.get_paths()["include"], MARSHAL_SOURCE, "-L", lib, f"-Wl,-rpath,{lib}",
+          "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-o", tmp], verbose)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, checks: bool = False) -> str:
     """Compile librelkl.so if any source is newer; returns its path.
 
@@ -52,17 +82,14 @@ def build(force: bool = False, verbose: bool = False, checks: bool = False) -> s
     that replays every tensor-core launch's schedule on the host first
     (relkl_check_schedule) and refuses a launch whose schedule is unsound."""
     checks = checks or os.environ.get("RELKL_CHECKS") == "1"
+    build_marshal(force, verbose)
     if not force and not checks and not _stale():
         return LIB
     tmp = LIB + ".tmp"
     cmd = [nvcc_path(), *NVCC_FLAGS, *(["-DRELKL_CHECKS"] if checks else []),
            "-I", os.path.join(ROOT, "include"),
            *[os.path.join(CSRC, f) for f in SOURCES], "-ldl", "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+    _run(cmd, verbose)
     os.replace(tmp, LIB)
     return LIB
 

@@ -20,12 +20,13 @@ __all__ = ["relkl_quantize_rows", "relkl_matmul_i8", "relkl_linear_i8"]
 
 def _matrix(x: torch.Tensor, what: str) -> Tuple[int, int, int]:
     """(rows, K, row stride) of x [..., K], whose rows must follow one another evenly."""
-    if x.dim() < 1:
+    dims = x.dim()
+    if dims < 1:
         raise ValueError(f"{what} must have at least one dimension")
     K = x.shape[-1]
     if K > 1 and x.stride(-1) != 1:
         raise ValueError(f"{what}'s last dimension must be contiguous")
-    if x.dim() == 2:
+    if dims == 2:
         rows, stride = x.shape[0], x.stride(0)
     elif x.is_contiguous():
         rows, stride = x.numel() // K if K else 0, K
@@ -64,9 +65,12 @@ def _record(device: torch.device, ws: Optional[torch.Tensor]) -> torch.Tensor:
         if ws.device != device:
             raise ValueError("ws must be on the inputs' device")
         return ws
-    if device.index not in _WS and torch.cuda.is_current_stream_capturing():
-        raise RuntimeError("call workspace(device) before capturing the first call of a device")
-    return workspace(device)
+    ws = _WS.get(device.index)
+    if ws is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("call workspace(device) before capturing the first call of a device")
+        ws = workspace(device)
+    return ws
 
 
 def _output(out: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.device):

@@ -8,28 +8,19 @@ from __future__ import annotations
 
 import math
 import struct
-from itertools import chain, repeat
-from operator import attrgetter, is_
-from typing import List, NamedTuple, Optional, Sequence, Union
+from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
 
 from . import _abi
 from ._abi import check
-from .ops import _DTYPES, _on
+from .ops import _on
 
 __all__ = ["AdamWState", "adamw_state", "relkl_adamw", "relkl_grad_norm", "AdamW"]
 
 BLOCK = 256     # elements that share one scale of an 8-bit state
 _E4M3 = torch.float8_e4m3fn
-# The layouts of the structs in include/relkl.h.  A relkl_adamw_tensor is packed as ten words:
-# seven pointers, the size, the two types, and the weight decay with the reserved zero.
-_TENSOR_WORDS = 10
-_PLAN = struct.Struct("@iiddddqPPP")
-_NORM = struct.Struct("@Pqii")
-
-_ptr, _numel, _device = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device
-_dtype, _shape = attrgetter("dtype"), attrgetter("shape")
+_PLAN = struct.Struct("@iiddddqPPP")     # relkl_adamw_plan (include/relkl.h)
 
 
 class AdamWState(NamedTuple):
@@ -57,31 +48,6 @@ def adamw_state(param: torch.Tensor, bits: int = 32) -> AdamWState:
                         for _ in range(2)))
 
 
-def _same_device(index: int, ts: Sequence[torch.Tensor]) -> None:
-    if set(map(_device, ts)) - {index}:
-        raise ValueError("all tensors must be CUDA tensors on one device (there is no CPU path)")
-    if not all(map(torch.Tensor.is_contiguous, ts)):
-        raise ValueError("tensors must be contiguous")
-
-
-def _decay_word(x: float) -> int:
-    return struct.unpack("=q", struct.pack("=fi", x, 0))[0]
-
-
-def _table(grads, params, copies, m, v, m_scale, v_scale, sizes, grad_types, param_types, decay) -> bytes:
-    """relkl_adamw_tensor records; the pointers and types as integers."""
-    types = [g | (p << 32) for g, p in zip(grad_types, param_types)]
-    words = chain.from_iterable(zip(grads, params, copies, m, v, m_scale, v_scale, sizes, types, decay))
-    return struct.pack(f"={_TENSOR_WORDS * len(sizes)}q", *words)
-
-
-def _types(ts: Sequence[torch.Tensor], what: str) -> List[int]:
-    try:
-        return [_DTYPES[t] for t in map(_dtype, ts)]
-    except KeyError as e:
-        raise TypeError(f"{what} must be bfloat16 or float32, not {e.args[0]}") from None
-
-
 def _scalar(x: torch.Tensor, dtype: torch.dtype, index: int, what: str) -> int:
     if x.dtype != dtype or x.numel() != 1 or x.get_device() != index:
         raise ValueError(f"{what} must be one {dtype} number on the parameters' device")
@@ -103,54 +69,9 @@ def relkl_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     that receive the new parameters rounded.  ``grad_scale``, one float32 number on the
     device, multiplies the gradients; where it is not finite nothing is written at all.
     """
-    n = len(params)
-    if len(grads) != n or len(states) != n or (copies is not None and len(copies) != n):
-        raise ValueError("params, grads, states and copies need one entry for each tensor")
-    decay = [weight_decay] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
-    if len(decay) != n:
-        raise ValueError("weight_decay needs one number, or one for each tensor")
-    if n == 0:
+    if len(params) == 0 and len(grads) == 0 and len(states) == 0:
         return
-    index = params[0].get_device()
-    if index < 0:
-        raise ValueError("params must be CUDA tensors (there is no CPU path)")
-    m, v, m_scale, v_scale = zip(*states)
-    kinds = list(map(_dtype, m))
-    if len(set(kinds)) > 1:       # one call for each kind of state
-        for kind in dict.fromkeys(kinds):
-            at = [k for k in range(n) if kinds[k] == kind]
-            pick = lambda xs: [xs[k] for k in at]  # noqa: E731
-            relkl_adamw(pick(params), pick(grads), pick(states), lr=lr, step=step, betas=betas,
-                        eps=eps, weight_decay=pick(decay),
-                        copies=None if copies is None else pick(copies), grad_scale=grad_scale,
-                        stream=stream)
-        return
-    if kinds[0] not in (torch.float32, _E4M3) or set(map(_dtype, v)) != {kinds[0]}:
-        raise TypeError("m and v must both be float32, or both float8_e4m3fn")
-    bits = 32 if kinds[0] == torch.float32 else 8
-    shapes = list(map(_shape, params))
-    every = [*params]
-    for xs in (grads, m, v) if copies is None else (grads, m, v, copies):
-        if list(map(_shape, xs)) != shapes:
-            raise ValueError("a parameter's gradient, states and copy must have its shape")
-        every += xs
-    sizes = list(map(_numel, params))
-    if bits == 8:
-        scales = m_scale + v_scale
-        if any(map(is_, scales, repeat(None))):
-            raise ValueError("8-bit states need their scales")
-        blocks = [-(-k // BLOCK) for k in sizes]
-        if set(map(_dtype, scales)) != {torch.float32} or list(map(_numel, scales)) != blocks + blocks:
-            raise ValueError("8-bit states need a float32 scale for each 256 elements")
-        every += scales
-        m_scale, v_scale = map(_ptr, m_scale), map(_ptr, v_scale)
-    else:
-        if not all(map(is_, m_scale + v_scale, repeat(None))):
-            raise ValueError("float32 states have no scales")
-        m_scale = v_scale = repeat(0)
-    _same_device(index, every)
-    if copies is not None and set(map(_dtype, copies)) != {torch.bfloat16}:
-        raise TypeError("copies must be bfloat16")
+    index, groups = _abi.marshal().adamw(params, grads, states, copies, weight_decay)
     lr_ptr = step_ptr = scale_ptr = 0
     if isinstance(lr, torch.Tensor):
         lr, lr_ptr = 0.0, _scalar(lr, torch.float32, index, "lr")
@@ -158,20 +79,13 @@ def relkl_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         step, step_ptr = 1, _scalar(step, torch.int64, index, "step")
     if grad_scale is not None:
         scale_ptr = _scalar(grad_scale, torch.float32, index, "grad_scale")
-    if isinstance(weight_decay, (int, float)):
-        decay = repeat(_decay_word(weight_decay))
-    else:
-        decay = map(_decay_word, decay)
-    table = _table(map(_ptr, grads), map(_ptr, params),
-                   repeat(0) if copies is None else map(_ptr, copies), map(_ptr, m), map(_ptr, v),
-                   m_scale, v_scale, sizes, _types(grads, "gradients"), _types(params, "parameters"),
-                   decay)
-    plan = _PLAN.pack(bits, 0, lr, betas[0], betas[1], eps, step, lr_ptr, step_ptr, scale_ptr)
     with _on(params[0].device, stream) as handle:
-        check(_abi.lib().relkl_adamw(n, table, plan, handle), "relkl_adamw")
-    # what autograd saved of the old values is no longer valid
-    written = params if copies is None else [*params, *copies]
-    torch.autograd.graph.increment_version([x for x in written if not x.is_inference()])
+        for bits, n, table in groups:      # float32 states, then those of 8 bits
+            plan = _PLAN.pack(bits, 0, lr, betas[0], betas[1], eps, step, lr_ptr, step_ptr, scale_ptr)
+            check(_abi.lib().relkl_adamw(n, table, plan, handle), "relkl_adamw")
+    _abi.marshal().written(params)
+    if copies is not None:
+        _abi.marshal().written(copies)
 
 
 def relkl_grad_norm(grads: Sequence[torch.Tensor], max_norm: float = math.inf, *,
@@ -180,20 +94,13 @@ def relkl_grad_norm(grads: Sequence[torch.Tensor], max_norm: float = math.inf, *
     together, and the factor min(1, max_norm / (norm + 1e-6)) that clips them to
     ``max_norm`` (NaN where the norm is not finite), for relkl_adamw's ``grad_scale``."""
     n = len(grads)
-    if n == 0:
-        raise ValueError("no gradients")
-    index = grads[0].get_device()
-    if index < 0:
-        raise ValueError("gradients must be CUDA tensors (there is no CPU path)")
-    _same_device(index, grads)
+    index, table = _abi.marshal().norm(grads)
     device = grads[0].device
     if out is not None and (out.dtype != torch.float32 or tuple(out.shape) != (2,) or
                             not out.is_contiguous() or out.get_device() != index):
         raise ValueError("out must be a contiguous float32 tensor of two numbers on the "
                          "gradients' device")
     lib = _abi.lib()
-    table = b"".join(map(_NORM.pack, map(_ptr, grads), map(_numel, grads),
-                         _types(grads, "gradients"), repeat(0)))
     nbytes = lib.relkl_grad_norm_bytes(n)
     with _on(device, stream) as handle:
         if out is None:

@@ -9,21 +9,15 @@ gives the token-major layout that ``relkl_weight_grad`` reads.
 from __future__ import annotations
 
 import math
-import struct
 from typing import List, NamedTuple, Optional, Sequence
 
 import torch
 
 from . import _abi
 from ._abi import check
-from .ops import _DTYPES, _cuda, _on
+from .ops import _DTYPES, _on
 
 __all__ = ["RotaryFreqs", "rotary_freqs", "relkl_rotary_qkv", "relkl_rotary", "Rotary", "rotary"]
-
-MAX_TENSORS = 3
-# the layouts of relkl_rotary_tensor and relkl_rotary_plan (include/relkl.h)
-_TENSOR = struct.Struct("@PP3q3qii")
-_PLAN = struct.Struct("@8iP2qifddP")
 
 
 class RotaryFreqs(NamedTuple):
@@ -81,16 +75,6 @@ def rotary_freqs(rot: int, base: float = 1e4, scaling: str = "none", factor: flo
     return RotaryFreqs(f.to(device), m)
 
 
-def _check_positions(positions: torch.Tensor, B: int, N: int, device: torch.device) -> torch.Tensor:
-    if positions.dtype not in (torch.int32, torch.int64) or positions.device != device:
-        raise ValueError("positions must be an int32 or int64 tensor on the inputs' device")
-    if tuple(positions.shape) == (N,):
-        positions = positions.unsqueeze(0).expand(B, N)
-    if tuple(positions.shape) != (B, N):
-        raise ValueError(f"positions must have shape ({B}, {N}) or ({N},)")
-    return positions
-
-
 def relkl_rotary_qkv(xs: Sequence[torch.Tensor], inv_freq: torch.Tensor, *,
                      apply: Optional[Sequence[bool]] = None, pos_scale: float = 1.0,
                      pos_offset: float = 0.0, positions: Optional[torch.Tensor] = None,
@@ -107,62 +91,25 @@ def relkl_rotary_qkv(xs: Sequence[torch.Tensor], inv_freq: torch.Tensor, *,
     tensor r to its output's layout and type.  ``out`` may have any non-overlapping
     strides and may be the inputs themselves; without it the outputs are contiguous
     tensors of ``out_dtype`` (default: the inputs' type)."""
-    n = len(xs)
-    if not 1 <= n <= MAX_TENSORS:
-        raise ValueError("1 to 3 tensors per call")
-    apply = (True,) * n if apply is None else tuple(apply)
-    if len(apply) != n or (out is not None and len(out) != n):
+    marshal = _abi.marshal()
+    marshal.rotary_inputs(xs, inv_freq)
+    if apply is not None and len(apply) != len(xs) or out is not None and len(out) != len(xs):
         raise ValueError("apply and out need one entry for each tensor")
     x0 = xs[0]
-    _cuda(x0, "x")
-    dev = x0.device
-    if x0.dim() != 4:
-        raise ValueError("expected [B, H, N, d] tensors")
-    if x0.dtype not in _DTYPES:
-        raise TypeError(f"unsupported dtype {x0.dtype}")
-    B, _, N, d = x0.shape
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or \
-            inv_freq.device != dev:
-        raise ValueError("inv_freq must be a contiguous float64 vector on the inputs' device")
-    rot = 2 * inv_freq.numel()
-    if rot > d:
-        raise ValueError(f"inv_freq has {rot // 2} pairs, more than a head of {d} holds")
-    for x in xs:
-        if x.dim() != 4 or x.dtype != x0.dtype or x.device != dev or \
-                (x.shape[0], x.shape[2], x.shape[3]) != (B, N, d):
-            raise ValueError("all tensors must share device, dtype, B, N and d")
-        if x.stride(3) != 1 and d > 1:
-            raise ValueError("the last dimension must be contiguous")
-    pos_ptr = pos_bytes = pos_b = pos_n = 0
-    if positions is not None:
-        positions = _check_positions(positions, B, N, dev)
-        pos_ptr = positions.data_ptr()
-        if pos_ptr:      # no token, nothing to read
-            pos_bytes = positions.element_size()
-            pos_b, pos_n = positions.stride()
-    with _on(dev, stream) as handle:
+    if out is None:
+        out_dtype = x0.dtype if out_dtype is None else out_dtype
+        if out_dtype not in _DTYPES:
+            raise TypeError(f"unsupported output dtype {out_dtype}")
+    elif out_dtype is not None and any(y.dtype != out_dtype for y in out):
+        raise ValueError(f"out must be {out_dtype} tensors")
+    with _on(x0.device, stream) as handle:
         if out is None:
-            out_dtype = x0.dtype if out_dtype is None else out_dtype
-            if out_dtype not in _DTYPES:
-                raise TypeError(f"unsupported output dtype {out_dtype}")
-            out = [torch.empty(x.shape, dtype=out_dtype, device=dev) for x in xs]
+            out = [torch.empty(x.shape, dtype=out_dtype, device=x0.device) for x in xs]
         else:
             out = list(out)
-            out_dtype = out[0].dtype if out_dtype is None else out_dtype
-            if out_dtype not in _DTYPES:
-                raise TypeError(f"unsupported output dtype {out_dtype}")
-            for x, y in zip(xs, out):
-                if y.shape != x.shape or y.dtype != out_dtype or y.device != dev or \
-                        (y.stride(3) != 1 and d > 1):
-                    raise ValueError(f"out must be {out_dtype} tensors of the inputs' shapes on "
-                                     f"{dev} whose last dimension is contiguous")
-        tensors = b"".join([
-            _TENSOR.pack(x.data_ptr(), y.data_ptr(), *x.stride()[:3], *y.stride()[:3], x.shape[1],
-                         bool(a)) for x, y, a in zip(xs, out, apply)])
-        plan = _PLAN.pack(B, N, d, rot, _DTYPES[x0.dtype], _DTYPES[out_dtype], bool(interleaved),
-                          bool(inverse), pos_ptr, pos_b, pos_n, pos_bytes, mscale, pos_scale,
-                          pos_offset, inv_freq.data_ptr())
-        check(_abi.lib().relkl_rotary(n, tensors, plan, handle), "relkl_rotary")
+        tensors, plan = marshal.rotary(xs, out, apply, inv_freq, positions, interleaved, inverse,
+                                       mscale, pos_scale, pos_offset)
+        check(_abi.lib().relkl_rotary(len(out), tensors, plan, handle), "relkl_rotary")
     return out
 
 

@@ -97,16 +97,8 @@ def test_norm_refusals():
     assert lib.relkl_grad_norm_bytes(1000) > need >= 8
 
 
-def test_binding_packs_the_structs():
+def test_binding_packs_the_plan():
     assert optim._PLAN.size == ctypes.sizeof(_abi.relkl_adamw_plan)
-    assert optim._NORM.size == ctypes.sizeof(_abi.relkl_norm_tensor)
-    table = optim._table([1, 11], [2, 12], [3, 13], [4, 14], [5, 15], [6, 16], [7, 17], [8, 18], [0, 1], [1, 0],
-                         [optim._decay_word(0.5), optim._decay_word(0.25)])
-    a, b = (_abi.relkl_adamw_tensor * 2).from_buffer_copy(table)
-    assert len(table) == ctypes.sizeof(_abi.relkl_adamw_tensor) * 2
-    assert (a.grad, a.param, a.copy, a.m, a.v, a.m_scale, a.v_scale, a.n) == (1, 2, 3, 4, 5, 6, 7, 8)
-    assert (a.grad_dtype, a.param_dtype, a.weight_decay, a.reserved) == (0, 1, 0.5, 0)
-    assert (b.v_scale, b.n, b.grad_dtype, b.param_dtype, b.weight_decay) == (17, 18, 1, 0, 0.25)
     p = _abi.relkl_adamw_plan.from_buffer_copy(optim._PLAN.pack(8, 0, 1.0, 2.0, 3.0, 4.0, 5, 6, 7, 8))
     assert (p.lr, p.eps, p.step, p.lr_dev, p.grad_scale) == (1.0, 4.0, 5, 6, 8)
 
@@ -120,6 +112,9 @@ def test_binding_checks_before_the_call():
         rk.relkl_adamw(p, [], s, lr=1e-3, step=1)
     with pytest.raises(ValueError, match="weight_decay"):
         rk.relkl_adamw(p, p, s, lr=1e-3, step=1, weight_decay=[0.1, 0.1])
+    for bad in ((1, p, s), (p, [None], s), (p, p, [None]), (p, p, [(p[0], p[0])])):
+        with pytest.raises((TypeError, ValueError)):
+            rk.relkl_adamw(*bad, lr=1e-3, step=1)
     with pytest.raises(ValueError, match="CUDA"):
         rk.relkl_grad_norm(p)
     with pytest.raises(ValueError, match="bits"):

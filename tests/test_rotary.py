@@ -83,24 +83,16 @@ def test_no_work_is_a_no_op():
     assert _call(_plan(), _tensor(x=None, y=None, H=0)) == _abi.RELKL_OK
 
 
-def test_binding_packs_the_structs():
-    from attention_relation_kl_b200 import positions as module
-    assert module._TENSOR.size == ctypes.sizeof(_abi.relkl_rotary_tensor)
-    assert module._PLAN.size == ctypes.sizeof(_abi.relkl_rotary_plan)
-    p = _abi.relkl_rotary_plan.from_buffer_copy(
-        module._PLAN.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13.0, 14.0, 15.0, 16))
-    assert (p.B, p.rot, p.inverse, p.positions, p.pos_stride[1], p.pos_bytes) == (1, 4, 8, 9, 11, 12)
-    assert (p.mscale, p.pos_scale, p.pos_offset, p.inv_freq) == (13.0, 14.0, 15.0, 16)
-
-
 def test_binding_checks_before_the_call():
     x = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         rk.relkl_rotary(x, torch.zeros(32, dtype=torch.float64))
     with pytest.raises(ValueError, match="1 to 3"):
         rk.relkl_rotary_qkv([], torch.zeros(32, dtype=torch.float64))
-    with pytest.raises(ValueError, match="one entry"):
-        rk.relkl_rotary_qkv([x, x], torch.zeros(32, dtype=torch.float64), apply=[True])
+    with pytest.raises(TypeError, match="tensors"):
+        rk.relkl_rotary_qkv([1], torch.zeros(32, dtype=torch.float64))
+    with pytest.raises(TypeError):
+        rk.relkl_rotary_qkv(x, None)
 
 
 def test_frequencies_follow_their_formulas():
