@@ -314,12 +314,100 @@ PyObject* rotary(PyObject*, PyObject* args) {
   });
 }
 
+[[noreturn]] void raise_about(PyObject* type, const char* what, const char* text) {
+  PyErr_Format(type, "%s %s", what, text);
+  throw Raised{};
+}
+
+// matrix(x, what) -> (rows, K, row stride, address, relkl_dtype, device index) of x [..., K],
+// whose rows must follow one another evenly
+PyObject* matrix(PyObject*, PyObject* args) {
+  return guarded([&]() -> PyObject* {
+    PyObject* o;
+    const char* what;
+    if (!PyArg_ParseTuple(args, "Os", &o, &what)) throw Raised{};
+    const at::Tensor& x = tensor(o, what);
+    if (!x.is_cuda()) raise_about(PyExc_ValueError, what, "must be a CUDA tensor (there is no CPU path)");
+    const int32_t type = element(x, what);
+    const int64_t dims = x.dim();
+    if (dims < 1) raise_about(PyExc_ValueError, what, "must have at least one dimension");
+    const int64_t K = x.size(dims - 1);
+    if (K > 1 && x.stride(dims - 1) != 1)
+      raise_about(PyExc_ValueError, what, "must have a contiguous last dimension");
+    if (K > 0x7fffffff) raise_about(PyExc_ValueError, what, "has rows of more than 2^31 - 1 elements");
+    int64_t rows = 1, stride = K, next = -1;   // next: the stride of a dimension around those seen
+    for (int64_t i = dims - 2; i >= 0; --i) {
+      const int64_t n = x.size(i);
+      rows *= n;
+      if (n <= 1) continue;
+      if (next < 0)
+        stride = x.stride(i);
+      else if (x.stride(i) != next)
+        raise_about(PyExc_ValueError, what, "must have rows that follow one another at one stride");
+      next = x.stride(i) * n;
+    }
+    return Py_BuildValue("(LLLKii)", static_cast<long long>(rows), static_cast<long long>(K),
+                         static_cast<long long>(stride),
+                         static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(x.const_data_ptr())),
+                         static_cast<int>(type), static_cast<int>(x.get_device()));
+  });
+}
+
+// codes(q, what, device index) -> (rows, K, row stride, address) of an int8 matrix laid out as
+// relkl_quantize_rows lays it out; index -1: any device
+PyObject* codes(PyObject*, PyObject* args) {
+  return guarded([&]() -> PyObject* {
+    PyObject* o;
+    const char* what;
+    int index;
+    if (!PyArg_ParseTuple(args, "Osi", &o, &what, &index)) throw Raised{};
+    const at::Tensor& q = tensor(o, what);
+    if (!q.is_cuda() || (index >= 0 && q.get_device() != index))
+      raise_about(PyExc_ValueError, what, "must be a CUDA tensor on the inputs' device (there is no CPU path)");
+    if (q.scalar_type() != at::kChar || q.dim() != 2)
+      raise_about(PyExc_ValueError, what, "must be an int8 matrix");
+    const int64_t rows = q.size(0), K = q.size(1);
+    int64_t stride = q.stride(0);
+    if (rows <= 1) stride = (K + 15) / 16 * 16;   // one row has no stride
+    const uintptr_t at = reinterpret_cast<uintptr_t>(q.const_data_ptr());
+    if ((K > 1 && q.stride(1) != 1) || stride % 16 || stride < K || at % 16)
+      raise_about(PyExc_ValueError, what,
+                  "must have contiguous rows that start at 16-byte boundaries, as relkl_quantize_rows "
+                  "lays them out");
+    return Py_BuildValue("(LLLK)", static_cast<long long>(rows), static_cast<long long>(K),
+                         static_cast<long long>(stride), static_cast<unsigned long long>(at));
+  });
+}
+
+// vector(v, n, what, device index) -> address of a float32 vector of n, 0 for None
+PyObject* vector(PyObject*, PyObject* args) {
+  return guarded([&]() -> PyObject* {
+    PyObject* o;
+    const char* what;
+    long long n;
+    int index;
+    if (!PyArg_ParseTuple(args, "OLsi", &o, &n, &what, &index)) throw Raised{};
+    if (o == Py_None) return PyLong_FromLong(0);
+    const at::Tensor& v = tensor(o, what);
+    if (v.scalar_type() != at::kFloat || v.dim() != 1 || v.numel() != n || !v.is_contiguous() || !v.is_cuda() ||
+        v.get_device() != index) {
+      PyErr_Format(PyExc_ValueError, "%s must be a contiguous float32 vector of %lld on the inputs' device",
+                   what, n);
+      throw Raised{};
+    }
+    return PyLong_FromVoidPtr(const_cast<void*>(v.const_data_ptr()));
+  });
+}
+
 PyMethodDef methods[] = {
     {"adamw", adamw, METH_VARARGS, "records of relkl_adamw"},
     {"written", written, METH_O, "marks tensors as changed in place"},
     {"norm", norm, METH_O, "records of relkl_grad_norm"},
     {"rotary_inputs", rotary_inputs, METH_VARARGS, "checks of relkl_rotary's inputs"},
     {"rotary", rotary, METH_VARARGS, "records of relkl_rotary"},
+    {"matrix", matrix, METH_VARARGS, "layout of a matrix of rows"},
+    {"codes", codes, METH_VARARGS, "layout of a matrix of codes"},
+    {"vector", vector, METH_VARARGS, "address of a float32 vector"},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,

@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import attention_relation_kl_b200 as rk
+from attention_relation_kl_b200 import _abi
 
 pytestmark = pytest.mark.gpu
 
@@ -229,6 +230,29 @@ def test_streams_and_captured_graphs(rows):
     torch.cuda.synchronize()
     for t, o in zip(xs, outs):
         assert torch.equal(o, rk.relkl_linear_i8(t, w, sw))
+
+
+# The two pair kernels.  A wait is tried for a hundred microseconds or so before its limit is
+# looked at, so the sums are as long as they may be: 300 us and more.
+@pytest.mark.parametrize("rows,cols,K", [(500, 4096, 131071), (5000, 1024, 131071)])
+def test_wait_that_runs_out_is_reported_and_the_context_survives(rows, cols, K):
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    q, s = rk.relkl_quantize_rows(torch.randn(rows, K, generator=gen, device="cuda").to(BF16))
+    w, sw = rk.relkl_quantize_rows(torch.randn(cols, K, generator=gen, device="cuda"))
+    ws = torch.empty(rk.relkl_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    rk.relkl_workspace_init(ws)
+    want = rk.relkl_matmul_i8(q, s, w, sw, ws=ws)
+    assert rk.relkl_get_device_error(ws) == (0, 0)
+    old = rk.relkl_set_wait_timeout_ns(0)
+    try:
+        rk.relkl_matmul_i8(q, s, w, sw, ws=ws)
+        code, where = rk.relkl_get_device_error(ws)
+    finally:
+        rk.relkl_set_wait_timeout_ns(old)
+    assert code == _abi.RELKL_ERR_TIMEOUT and where != 0
+    rk.relkl_workspace_init(ws)
+    assert torch.equal(rk.relkl_matmul_i8(q, s, w, sw, ws=ws), want)
+    assert rk.relkl_get_device_error(ws) == (0, 0)
 
 
 def test_bad_calls_are_refused():
