@@ -43,7 +43,8 @@ cudaError_t launch_grad_norm(const NormTensor* t, int n, int64_t chunks, int gri
 cudaError_t launch_norm_finish(const double* partial, int n, float max_norm, float* out,
                                cudaStream_t stream);
 cudaError_t launch_quantize_rows(const RowsParams& p, bool x_bf16, int num_sms, cudaStream_t stream);
-cudaError_t launch_gemv_i8(const GemvParams& p, bool x_bf16, bool y_bf16, cudaStream_t stream);
+cudaError_t launch_gemv_i8(const GemvParams& p, bool x_bf16, bool y_bf16, int num_sms,
+                           cudaStream_t stream);
 cudaError_t launch_gemm_i8(I8Params& p, const I8Call& c, bool y_bf16, int num_sms, cudaStream_t stream);
 using EncodeTiledFnG = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                     const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -1017,7 +1018,7 @@ relkl_status relkl_matmul_i8(int64_t rows, int32_t cols, int32_t K, const int8_t
                              int32_t y_dtype, int64_t y_stride, void* ws, size_t ws_bytes,
                              void* stream) {
   NvtxRange nvtx_range("relkl_matmul_i8");
-  if (!rows_ok(rows, K) || cols < 0) return RELKL_ERR_INVALID;
+  if (!rows_ok(rows, K) || cols < 0 || cols > (1 << 30)) return RELKL_ERR_INVALID;
   if (rows == 0 || cols == 0) return RELKL_OK;
   if (!codes_ok(q, q_stride, K) || !codes_ok(w, w_stride, K) || !matrix_ok(y, y_dtype, y_stride, cols) ||
       !q_scale || !w_scale || !aligned(q_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4))
@@ -1041,7 +1042,7 @@ relkl_status relkl_linear_i8(int64_t rows, int32_t cols, int32_t K, const void* 
                              int64_t y_stride, void* scratch, size_t scratch_bytes, void* ws,
                              size_t ws_bytes, void* stream) {
   NvtxRange nvtx_range("relkl_linear_i8");
-  if (!rows_ok(rows, K) || cols < 0) return RELKL_ERR_INVALID;
+  if (!rows_ok(rows, K) || cols < 0 || cols > (1 << 30)) return RELKL_ERR_INVALID;
   if (rows == 0 || cols == 0) return RELKL_OK;
   if (!matrix_ok(x, x_dtype, x_stride, K) || !codes_ok(w, w_stride, K) ||
       !matrix_ok(y, y_dtype, y_stride, cols) || !w_scale || !aligned(w_scale, 4) || !aligned(bias, 4))
@@ -1049,16 +1050,17 @@ relkl_status relkl_linear_i8(int64_t rows, int32_t cols, int32_t K, const void* 
   relkl_status s = check_ws(ws, ws_bytes);
   if (s != RELKL_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (few_rows(rows, K)) {
-    GemvParams p = {x, w, w_scale, bias, y, x_stride, w_stride, y_stride, static_cast<int>(rows),
-                    cols, K, wide_rows(x, x_dtype, x_stride)};
-    cudaError_t e = launch_gemv_i8(p, x_dtype == RELKL_BF16, y_dtype == RELKL_BF16, st);
-    return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
-  }
-  if (!scratch || !aligned(scratch, 16) || scratch_bytes < relkl_linear_i8_bytes(rows, K))
+  const bool few = few_rows(rows, K);
+  if (!few && (!scratch || !aligned(scratch, 16) || scratch_bytes < relkl_linear_i8_bytes(rows, K)))
     return RELKL_ERR_WORKSPACE;
   DevInfo dev;
   if ((s = device_info(&dev)) != RELKL_OK) return s;
+  if (few) {
+    GemvParams p = {x, w, w_scale, bias, y, x_stride, w_stride, y_stride, static_cast<int>(rows),
+                    cols, K, wide_rows(x, x_dtype, x_stride)};
+    cudaError_t e = launch_gemv_i8(p, x_dtype == RELKL_BF16, y_dtype == RELKL_BF16, dev.sms, st);
+    return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
+  }
   int8_t* q = static_cast<int8_t*>(scratch);
   const int64_t pitch = code_pitch(K);
   float* scale = reinterpret_cast<float*>(q + rows * pitch);

@@ -7,14 +7,19 @@
 // is exact in int32, so neither the split of K nor any order changes a bit;
 // it becomes float32 once, is scaled, and rounded once to the output's type.
 //
-// Three kernels:
-//   * relkl_quantize_rows_kernel: one pass over the rows; HBM.
+// Four kernels:
+//   * relkl_quantize_rows_kernel: one pass over the rows.  HBM: 32K x 4096 bf16
+//     in 61 to 68 us, 6.6 to 5.9 TB/s.
 //   * relkl_gemv_i8_kernel, up to kGemvRows rows: every CTA codes the rows for
 //     itself in shared memory (they are small and in L2) while its warps'
 //     weights are on the way, then one warp per channel sums with dp4a.  Bound
-//     by the weights' bytes, and at these sizes by the launch.
+//     by the launch and the weights' bytes: 1 x 4096 x 4096 in 4.8 us.
 //   * relkl_gemm_i8_kernel: tcgen05.mma kind::i8 (s8 x s8 -> s32) with both
-//     operands K-major in 128-byte swizzled shared memory, fed by TMA.
+//     operands K-major in 128-byte swizzled shared memory, fed by TMA; one tile
+//     for a CTA, or K split over a cluster, for tens to hundreds of rows.
+//   * relkl_gemm_i8_pair_kernel: the same by pairs of CTAs, persistent.  32K x
+//     4096 x 4096 in 337 us, 3.27 POP/s (99 % of twice the measured bf16 rate);
+//     a library product of the same codes to int32, without scales, takes 341.
 #include <algorithm>
 #include <cstdint>
 
@@ -195,6 +200,7 @@ __device__ __forceinline__ U from_float(float v) {
 
 // groups of eight of a row that one thread holds
 constexpr int kRowGroups = 4;
+constexpr int GEMV_THREADS = 512;
 
 // The largest magnitude among `warps` warps' (all of the block's threads call).
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* part) {
@@ -273,93 +279,127 @@ __global__ void __launch_bounds__(512, 2) relkl_quantize_rows_kernel(const RowsP
 }
 
 // ------------------------------------------------------------ few rows
-// Shared memory: the rows' codes, each padded with zeros to 16 bytes.
+// Every CTA codes the rows for itself, all R of them side by side: a group of
+// eight of each row to a thread, with three barriers whatever R is.  Shared
+// memory: the rows' codes, each padded with zeros to 16 bytes.
 template <typename T, typename U, int R>
-__global__ void __launch_bounds__(256) relkl_gemv_i8_kernel(const GemvParams p) {
+__global__ void __launch_bounds__(GEMV_THREADS, R > 4 ? 1 : 2) relkl_gemv_i8_kernel(const GemvParams p) {
+  constexpr int WARPS = GEMV_THREADS / 32;
   extern __shared__ __align__(16) int8_t codes[];
-  __shared__ uint32_t part[8];
-  __shared__ float scales[R];
+  __shared__ uint32_t part[R][WARPS], largest_of[R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  int64_t c = static_cast<int64_t>(blockIdx.x) * WARPS + warp;
   const int pitch = (p.K + 15) / 16 * 16;
-  const int vecs = p.K / 16;
-  const int8_t* w = p.w + (c < p.cols ? c : 0) * p.w_stride;
+  const int vecs = p.K / 16, groups = p.K / 8;
 
   // the first of the weights are on their way while the rows are coded
-  constexpr int AHEAD = 8;
+  constexpr int AHEAD = 4;
   uint4 first[AHEAD];
+  const int8_t* w = p.w + (c < p.cols ? c : 0) * p.w_stride;
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i)
     if (i * 32 + lane < vecs) first[i] = __ldcg(reinterpret_cast<const uint4*>(w) + i * 32 + lane);
 
-#pragma unroll 1
+  const T* x = static_cast<const T*>(p.x);
+  auto load = [&](Held<T>& h, int r, int g) {
+    const T* at = x + r * p.x_stride + 8 * g;
+    p.wide ? h.load(at) : h.load_any(at);
+  };
+  Held<T> mine[R];
+  const int me = threadIdx.x;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < p.rows && me < groups) load(mine[r], r, me);
+#pragma unroll
   for (int r = 0; r < R; ++r) {
     if (r >= p.rows) break;
-    const T* x = static_cast<const T*>(p.x) + r * p.x_stride;
-    uint32_t most = 0;
-    const int groups = p.K / 8;
-    for (int g = threadIdx.x; g < groups; g += 256) {
+    uint32_t most = me < groups ? largest(mine[r], 0u) : 0u;
+    for (int g = GEMV_THREADS + me; g < groups; g += GEMV_THREADS) {
       Held<T> h;
-      p.wide ? h.load(x + 8 * g) : h.load_any(x + 8 * g);
+      load(h, r, g);
       most = largest(h, most);
     }
-    for (int i = 8 * groups + threadIdx.x; i < p.K; i += 256)
-      most = largest(x[i], most);
-    __syncthreads();          // the last row's maxima have been read
-    const RowCoder coder(block_max(largest_bits<T>(most), part));
+    if (8 * groups + me < p.K) most = largest(x[r * p.x_stride + 8 * groups + me], most);
+    most = warp_max(largest_bits<T>(most));
+    if (lane == 0) part[r][warp] = most;
+  }
+  __syncthreads();
+  if (warp < R && warp < p.rows) {
+    const uint32_t most = warp_max(lane < WARPS ? part[warp][lane] : 0u);
+    if (lane == 0) largest_of[warp] = most;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (r >= p.rows) break;
+    const RowCoder coder(largest_of[r]);
     int8_t* q = codes + r * pitch;
-    for (int g = threadIdx.x; g < groups; g += 256) {
-      Held<T> h;
-      p.wide ? h.load(x + 8 * g) : h.load_any(x + 8 * g);
+    auto put = [&](const Held<T>& h, int g) {
       bool again;
       *reinterpret_cast<uint2*>(q + 8 * g) = coder.codes(h, again);
       if (again)
 #pragma unroll 1
-        for (int k = 8 * g; k < 8 * g + 8; ++k) q[k] = static_cast<int8_t>(coder.code(to_float(x[k])));
+        for (int k = 8 * g; k < 8 * g + 8; ++k) q[k] = static_cast<int8_t>(coder.code(to_float(x[r * p.x_stride + k])));
+    };
+    if (me < groups) put(mine[r], me);
+    for (int g = GEMV_THREADS + me; g < groups; g += GEMV_THREADS) {
+      Held<T> h;
+      load(h, r, g);
+      put(h, g);
     }
-    for (int i = 8 * groups + threadIdx.x; i < pitch; i += 256)
-      q[i] = i < p.K ? static_cast<int8_t>(coder.code(to_float(x[i]))) : 0;
-    if (threadIdx.x == 0) scales[r] = coder.scale();
+    const int i = 8 * groups + me;       // the rest of the row, and its padding
+    if (i < pitch) q[i] = i < p.K ? static_cast<int8_t>(coder.code(to_float(x[r * p.x_stride + i]))) : 0;
   }
   __syncthreads();
-  if (c >= p.cols) return;
 
-  int acc[R];
+  for (; c < p.cols; c += static_cast<int64_t>(gridDim.x) * WARPS) {
+    w = p.w + c * p.w_stride;
+    int acc[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) acc[r] = 0;
-  auto add = [&](const uint4& a, int at) {
+    for (int r = 0; r < R; ++r) acc[r] = 0;
+    auto add = [&](const uint4& a, int at) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= p.rows) break;
+        const uint4 b = *reinterpret_cast<const uint4*>(codes + r * pitch + at);
+        acc[r] = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), acc[r]);
+        acc[r] = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), acc[r]);
+        acc[r] = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), acc[r]);
+        acc[r] = __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), acc[r]);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (i * 32 + lane < vecs) add(first[i], 16 * (i * 32 + lane));
+#pragma unroll 4
+    for (int i = AHEAD * 32 + lane; i < vecs; i += 32)
+      add(__ldcg(reinterpret_cast<const uint4*>(w) + i), 16 * i);
+    // the bytes behind the last whole vector, one to a lane
+    if (16 * vecs + lane < p.K) {
+      const int b = w[16 * vecs + lane];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < p.rows) acc[r] += b * codes[r * pitch + 16 * vecs + lane];
+    }
+    // the next channel's first weights
+    const int64_t next = c + static_cast<int64_t>(gridDim.x) * WARPS;
+    if (next < p.cols) {
+      const uint4* n = reinterpret_cast<const uint4*>(p.w + next * p.w_stride);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (i * 32 + lane < vecs) first[i] = __ldcg(n + i * 32 + lane);
+    }
+    int mine_of = 0;                     // lane r: row r's sum
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (r >= p.rows) break;
-      const uint4 b = *reinterpret_cast<const uint4*>(codes + r * pitch + at);
-      acc[r] = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), acc[r]);
-      acc[r] = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), acc[r]);
-      acc[r] = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), acc[r]);
-      acc[r] = __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), acc[r]);
+      const int sum = __reduce_add_sync(0xffffffffu, acc[r]);
+      if (lane == r) mine_of = sum;
     }
-  };
-#pragma unroll
-  for (int i = 0; i < AHEAD; ++i)
-    if (i * 32 + lane < vecs) add(first[i], 16 * (i * 32 + lane));
-#pragma unroll 4
-  for (int i = AHEAD * 32 + lane; i < vecs; i += 32)
-    add(__ldcg(reinterpret_cast<const uint4*>(w) + i), 16 * i);
-  // the bytes behind the last whole vector, one to a lane
-  if (16 * vecs + lane < p.K) {
-    const int b = w[16 * vecs + lane];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (r < p.rows) acc[r] += b * codes[r * pitch + 16 * vecs + lane];
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r) acc[r] = __reduce_add_sync(0xffffffffu, acc[r]);
-  if (lane == 0) {
-    const float sw = p.w_scale[c], b = p.bias ? p.bias[c] : 0.0f;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (r < p.rows)
-        static_cast<U*>(p.y)[r * p.y_stride + c] =
-            from_float<U>(fmaf(static_cast<float>(acc[r]), scales[r] * sw, b));
+    if (lane < R && lane < p.rows) {
+      const float s = RowCoder(largest_of[lane]).scale() * p.w_scale[c];
+      static_cast<U*>(p.y)[lane * p.y_stride + c] =
+          from_float<U>(fmaf(static_cast<float>(mine_of), s, p.bias ? p.bias[c] : 0.0f));
+    }
   }
 }
 
@@ -749,8 +789,11 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
 // 128 rows of q and half of the channels' codes, so an SM reads (128 + BN / 2)
 // x 32 bytes of shared memory for an instruction where one CTA by itself reads
 // (128 + BN) x 32; at the int8 rate the latter needs more than the 128 bytes a
-// clock that an SM has.  Persistent; the sums of one tile are read from TMEM
-// while the next one's are formed.
+// clock that an SM has (32K x 4096 x 4096: 936 us with its coding, then 437).
+// Persistent; the sums of one tile are read from TMEM while the next one's are
+// formed.  What the tiles fetch from L2, 15 TB/s, is next to bound it: results
+// that left lane by lane (32 bytes of a row each) cost 372 us, as whole lines
+// by TMA 337.
 namespace i8 {
 
 // warp 0 TMA, warp 1 MMA, warps 2-9 epilogue: two for each quarter of the
@@ -1104,21 +1147,24 @@ cudaError_t launch_quantize_rows(const RowsParams& p, bool x_bf16, int num_sms, 
 namespace {
 
 template <typename T, typename U, int R>
-cudaError_t gemv(const GemvParams& p, cudaStream_t stream) {
+cudaError_t gemv(const GemvParams& p, int num_sms, cudaStream_t stream) {
   const int smem = p.rows * ((p.K + 15) / 16 * 16);
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024)
     e = cudaFuncSetAttribute(relkl_gemv_i8_kernel<T, U, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  relkl_gemv_i8_kernel<T, U, R><<<(p.cols + 7) / 8, 256, smem, stream>>>(p);
+  // as many CTAs as the SMs hold at a time: more would code the rows once more
+  const int need = (p.cols + GEMV_THREADS / 32 - 1) / (GEMV_THREADS / 32);
+  const int most = num_sms * (R > 4 ? 1 : 2);
+  relkl_gemv_i8_kernel<T, U, R><<<need < most ? need : most, GEMV_THREADS, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, typename U>
-cudaError_t gemv_rows(const GemvParams& p, cudaStream_t stream) {
-  if (p.rows == 1) return gemv<T, U, 1>(p, stream);
-  if (p.rows <= 4) return gemv<T, U, 4>(p, stream);
-  return gemv<T, U, kGemvRows>(p, stream);
+cudaError_t gemv_rows(const GemvParams& p, int num_sms, cudaStream_t stream) {
+  if (p.rows == 1) return gemv<T, U, 1>(p, num_sms, stream);
+  if (p.rows <= 4) return gemv<T, U, 4>(p, num_sms, stream);
+  return gemv<T, U, kGemvRows>(p, num_sms, stream);
 }
 
 // K-major codes [rows, K] of `stride` bytes a row, as boxes of 128 bytes x `box` rows
@@ -1229,10 +1275,10 @@ cudaError_t gemm_pick(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
 
 }  // namespace
 
-cudaError_t launch_gemv_i8(const GemvParams& p, bool x_bf16, bool y_bf16, cudaStream_t stream) {
+cudaError_t launch_gemv_i8(const GemvParams& p, bool x_bf16, bool y_bf16, int num_sms, cudaStream_t stream) {
   using H = __nv_bfloat16;
-  if (x_bf16) return y_bf16 ? gemv_rows<H, H>(p, stream) : gemv_rows<H, float>(p, stream);
-  return y_bf16 ? gemv_rows<float, H>(p, stream) : gemv_rows<float, float>(p, stream);
+  if (x_bf16) return y_bf16 ? gemv_rows<H, H>(p, num_sms, stream) : gemv_rows<H, float>(p, num_sms, stream);
+  return y_bf16 ? gemv_rows<float, H>(p, num_sms, stream) : gemv_rows<float, float>(p, num_sms, stream);
 }
 
 cudaError_t launch_gemm_i8(I8Params& p, const I8Call& c, bool y_bf16, int num_sms, cudaStream_t stream) {

@@ -469,8 +469,8 @@ relkl_status relkl_grad_norm(int32_t n_tensors, const relkl_norm_tensor* tensors
  * row stride in bytes that is a multiple of 16 and at least K, at 16-byte
  * aligned addresses; what lies between K and the stride is not read.  x and y
  * are row-major with any stride of at least K (cols) elements, at addresses
- * aligned to their type.  rows, cols >= 0; with rows or cols 0 a call is a
- * no-op.  q_scale, w_scale and bias are float, 4-byte aligned; bias may be
+ * aligned to their type.  rows >= 0, 0 <= cols <= 2^30; with rows or cols 0 a
+ * call is a no-op.  q_scale, w_scale and bias are float, 4-byte aligned; bias may be
  * NULL.  No output may overlap an input (unchecked for rows of strided views).
  */
 
@@ -490,7 +490,7 @@ relkl_status relkl_matmul_i8(int64_t rows, int32_t cols, int32_t K, const int8_t
                              int32_t y_dtype, int64_t y_stride, void* ws, size_t ws_bytes,
                              void* stream);
 
-/* relkl_quantize_rows of x and the product with its codes.  Up to 8 rows (of at
+/* relkl_quantize_rows of x and the product with its codes.  Up to 6 rows (of at
  * most 98,304 bytes of codes together) take one kernel for both; more are coded
  * into scratch first: relkl_linear_i8_bytes(rows, K) bytes of device memory
  * (0 for few rows), 16-byte aligned, used by this call's work only.          */

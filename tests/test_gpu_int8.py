@@ -100,8 +100,8 @@ def test_codes_of_ties_extremes_and_rows_without_a_scale(dtype):
     # products of such rows: NaN for the whole row, the bias for a row of zeros
     w, sw = _weights(9, K)
     bias = _randn((9,), F32, 3)
-    y = rk.relkl_linear_i8(x[:8], w, sw, bias=bias, out_dtype=F32)
     z = rk.relkl_linear_i8(x, w, sw, bias=bias, out_dtype=F32)
+    y = torch.cat([rk.relkl_linear_i8(x[k:k + 4], w, sw, bias=bias, out_dtype=F32) for k in (0, 4)])
     for t in (y, z[:8]):
         assert torch.isnan(t[3:6]).all() and torch.equal(t[6], bias)
         assert torch.isfinite(t[[0, 7]]).all()
@@ -122,7 +122,7 @@ def test_codes_of_every_pair_of_bf16_mantissas(dtype):
         assert np.array_equal(_np(q), _codes(y)[0])
 
 
-ROWS = [1, 2, 4, 5, 8, 9, 16, 77, 128, 129, 300]
+ROWS = [1, 2, 4, 5, 6, 7, 8, 9, 16, 77, 128, 129, 300]
 
 
 @pytest.mark.parametrize("cols,K", [(1, 1), (7, 17), (64, 128), (65, 100), (200, 129), (1000, 64), (33, 4096),
