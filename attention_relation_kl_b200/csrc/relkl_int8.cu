@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(512, 2) relkl_quantize_rows_kernel(const RowsP
 // eight of each row to a thread, with three barriers whatever R is.  Shared
 // memory: the rows' codes, each padded with zeros to 16 bytes.
 template <typename T, typename U, int R>
-__global__ void __launch_bounds__(GEMV_THREADS, R > 4 ? 1 : 2) relkl_gemv_i8_kernel(const GemvParams p) {
+__global__ void __launch_bounds__(GEMV_THREADS, 2) relkl_gemv_i8_kernel(const GemvParams p) {
   constexpr int WARPS = GEMV_THREADS / 32;
   extern __shared__ __align__(16) int8_t codes[];
   __shared__ uint32_t part[R][WARPS], largest_of[R];
@@ -671,9 +671,10 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
       uint32_t arms[S::STAGES] = {};
       // the weights of the first stages, which no kernel before this one
       // writes, are on their way while the rows are still being coded
+      const uint32_t stage_bytes = p.a_box * BK + S::B_BYTES;
       const int early = min(k1 - k0, S::STAGES);
       for (int it = 0; it < early; ++it) {
-        mbar_arrive_expect_tx(FULL(it), S::STAGE);
+        mbar_arrive_expect_tx(FULL(it), stage_bytes);
         tma_load_2d(base + it * S::STAGE + S::A_BYTES, &p.tm_b, FULL(it), (k0 + it) * BK, nt * BN);
         ++arms[it];
       }
@@ -684,7 +685,7 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
         const int s = it % S::STAGES;
         if (!mbar_wait(EMPTY(s), ((it / S::STAGES) & 1) ^ 1, wc, W_TMA_EMPTY_J)) break;
         const uint32_t a = base + s * S::STAGE;
-        mbar_arrive_expect_tx(FULL(s), S::STAGE);
+        mbar_arrive_expect_tx(FULL(s), stage_bytes);
         tma_load_2d(a, &p.tm_a, FULL(s), kc * BK, mt * BM);
         tma_load_2d(a + S::A_BYTES, &p.tm_b, FULL(s), kc * BK, nt * BN);
         ++arms[s];
@@ -1155,7 +1156,7 @@ cudaError_t gemv(const GemvParams& p, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // as many CTAs as the SMs hold at a time: more would code the rows once more
   const int need = (p.cols + GEMV_THREADS / 32 - 1) / (GEMV_THREADS / 32);
-  const int most = num_sms * (R > 4 ? 1 : 2);
+  const int most = num_sms * 2;
   relkl_gemv_i8_kernel<T, U, R><<<need < most ? need : most, GEMV_THREADS, smem, stream>>>(p);
   return cudaGetLastError();
 }
@@ -1163,7 +1164,6 @@ cudaError_t gemv(const GemvParams& p, int num_sms, cudaStream_t stream) {
 template <typename T, typename U>
 cudaError_t gemv_rows(const GemvParams& p, int num_sms, cudaStream_t stream) {
   if (p.rows == 1) return gemv<T, U, 1>(p, num_sms, stream);
-  if (p.rows <= 4) return gemv<T, U, 4>(p, num_sms, stream);
   return gemv<T, U, kGemvRows>(p, num_sms, stream);
 }
 
@@ -1213,7 +1213,12 @@ template <int BN, typename U>
 cudaError_t gemm(I8Params& p, const I8Call& c, cudaStream_t stream) {
   using S = i8::Smem<BN>;
   p.m_tiles = static_cast<int>((p.rows + i8::BM - 1) / i8::BM);
-  if (!encode_codes(&p.tm_a, c.q, p.rows, c.K, c.q_stride, i8::BM, c.encode) ||
+  // A box of rows only as high as there are rows (in eights, the swizzle's
+  // period): filling the rest of 128 with zeros costs more than reading them
+  // would, 27 us instead of 18 for 9 x 8192 x 8192.  The rows behind the box
+  // hold whatever the stage held; their sums are not stored.
+  p.a_box = p.rows < i8::BM ? static_cast<int>((p.rows + 7) / 8 * 8) : i8::BM;
+  if (!encode_codes(&p.tm_a, c.q, p.rows, c.K, c.q_stride, p.a_box, c.encode) ||
       !encode_codes(&p.tm_b, c.w, p.cols, c.K, c.w_stride, BN, c.encode))
     return cudaErrorInvalidValue;
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * ((p.cols + BN - 1) / BN);
@@ -1243,15 +1248,16 @@ cudaError_t gemm_pair(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
   return launch_cluster(kernel, p, 2 * pairs, i8::PAIR_THREADS, 2, S::ALLOC, c.after_rows, stream);
 }
 
-// Four kernels by the width of their tiles, the one with the least estimated
-// time: waves of tiles times the time of one wave, as measured relative to one
-// another (K = 4096, full waves: 9.3, 11.5, 10.0 and 13.8 us; K = 512: 4.4, 5.2,
-// 5.9 and 7.6 us).  So 128 rows x 4096 channels take 64 columns a tile (10.6
-// us; the others 11.3, 12.0, 15.4), 500 rows pairs with 128 columns (12.6; 64
-// columns 20.4, pairs with 256 16.0), 1000 rows pairs with 256 (16.9; 38.3,
-// 23.1, 21.2).  Where tiles of 64 columns leave SMs idle, K is split over up to
-// four of them: 16 rows x 1024 channels 9.8 us alone, 8.8 and 6.9 us with two
-// and four shares, 11.0 us with eight.
+// Four ways by the width of a tile, the one with the least estimated time:
+// waves of tiles times the time of one wave, as measured (K = 4096, full
+// waves: 9.3 us with one CTA and 64 columns, 11.0 with 128; pairs 8.5 with 128
+// columns, 11.3 with 256; a single wave 10.9, 11.6, 11.6 and 15.0 us, so that
+// pairs with 128 are counted as 9.5).  128 and 256 rows x 4096 channels take 64
+// columns a tile (10.4 and 11.0 us; the others 11.6 to 15), 500 rows pairs with
+// 128 (12.3; 64 columns 20.6, pairs with 256 15.3), 1000 rows pairs with 256
+// (16.3; 38, 23 and 20).  Where tiles of 64 columns leave SMs idle, K is split
+// over up to four of them: 16 rows x 1024 channels 10.0 us alone, 8.9 and 6.9 us
+// with two and four shares, 11.3 us with eight.
 template <typename U>
 cudaError_t gemm_pick(I8Params& p, const I8Call& c, int num_sms, cudaStream_t stream) {
   p.k_chunks = (c.K + i8::BK - 1) / i8::BK;
@@ -1260,9 +1266,9 @@ cudaError_t gemm_pick(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
   auto cost = [&](int64_t n, int at_once, int wave) { return (n + at_once - 1) / at_once * wave; };
   const int pairs = num_sms / 2;
   const int64_t t64 = tiles(i8::BM, 64);
-  const int64_t one64 = cost(t64, num_sms, 93), one128 = cost(tiles(i8::BM, 128), num_sms, 115);
-  const int64_t two128 = cost(tiles(2 * i8::BM, 128), pairs, 100);
-  const int64_t two256 = cost(tiles(2 * i8::BM, 256), pairs, 138);
+  const int64_t one64 = cost(t64, num_sms, 93), one128 = cost(tiles(i8::BM, 128), num_sms, 110);
+  const int64_t two128 = cost(tiles(2 * i8::BM, 128), pairs, 95);
+  const int64_t two256 = cost(tiles(2 * i8::BM, 256), pairs, 115);
   const int64_t least = std::min(std::min(one64, one128), std::min(two128, two256));
   if (two256 == least) return gemm_pair<256, U>(p, c, num_sms, stream);
   if (one64 == least) {

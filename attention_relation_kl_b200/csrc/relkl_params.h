@@ -161,11 +161,11 @@ struct NormParams {
 };
 
 // Products in 8-bit integers: row codes, few rows, and the tensor-core product.
-// Most rows of the kernel for few rows.  Against coding and product as two
-// kernels, K x channels: 4096 x 4096, 1 row 4.8 and 15 us, 4 rows 9.4 and 15,
-// 5 rows 10.2 and 14, 8 rows 13.7 and 14; 1024 x 1024, 5 rows 5.6 and 9; 8192 x
-// 8192, 5 rows 28 and 31 us, 8 rows 37 and 31 us.
-constexpr int kGemvRows = 6;
+// Most rows of the kernel for few rows.  Against the tensor cores (coding and
+// product, the second started early), K x channels: 4096 x 4096, 1, 2, 4 and 5
+// rows 4.9, 6.3, 9.4 and 10.8 us, there 9.9 us; 1024 x 1024, 4 rows 5.0, there
+// 7.2; 8192 x 8192, 2, 4 and 5 rows 13, 21 and 28, there 19 us.
+constexpr int kGemvRows = 4;
 constexpr int kGemvBytes = 96 * 1024; // most bytes of their codes in shared memory
 
 struct RowsParams {
@@ -188,7 +188,7 @@ struct GemvParams {
 };
 
 struct I8Params {
-  CUtensorMap tm_a;                   // codes [rows, K]: box 128 bytes x 128 rows, 128B swizzle
+  CUtensorMap tm_a;                   // codes [rows, K]: box 128 bytes x up to 128 rows, 128B swizzle
   CUtensorMap tm_b;                   // weights [cols, K]: box 128 bytes x BN rows
   CUtensorMap tm_y;                   // y: box 128 bytes x 32 rows, 128B swizzle (pairs, y_wide)
   const float *x_scale, *w_scale, *bias;
@@ -197,6 +197,7 @@ struct I8Params {
   int cols;
   int y_wide;                         // rows of y start at 16-byte (1) or 32-byte (2) boundaries
   int m_tiles, n_tiles, n_units, k_chunks, split;   // set by the launch
+  int a_box;                          // rows of tm_a's box (one CTA for a tile)
   DevStatus* status;
   unsigned long long timeout_ns;
 };

@@ -106,7 +106,7 @@ def relkl_linear_i8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
                     stream=None) -> torch.Tensor:
     """x [..., K] (bf16 or float32) through a projection in 8 bits: its rows are coded as by
     relkl_quantize_rows and multiplied with the codes w [cols, K] as by relkl_matmul_i8.
-    Returns [..., cols] of ``out_dtype`` (x's type without it); one kernel for up to 6 rows.
+    Returns [..., cols] of ``out_dtype`` (x's type without it); one kernel for up to 4 rows.
     ``out`` may have rows at any one stride; its addresses may not meet an input's."""
     m = _abi.marshal()
     rows, K, stride, x_ptr, x_type, index = m.matrix(x, "x")

@@ -490,7 +490,7 @@ relkl_status relkl_matmul_i8(int64_t rows, int32_t cols, int32_t K, const int8_t
                              int32_t y_dtype, int64_t y_stride, void* ws, size_t ws_bytes,
                              void* stream);
 
-/* relkl_quantize_rows of x and the product with its codes.  Up to 6 rows (of at
+/* relkl_quantize_rows of x and the product with its codes.  Up to 4 rows (of at
  * most 98,304 bytes of codes together) take one kernel for both; more are coded
  * into scratch first: relkl_linear_i8_bytes(rows, K) bytes of device memory
  * (0 for few rows), 16-byte aligned, used by this call's work only.          */

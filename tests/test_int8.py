@@ -68,8 +68,8 @@ def test_no_rows_or_channels_are_no_ops():
 
 def test_scratch_sizes():
     b = _abi.lib().relkl_linear_i8_bytes
-    assert b(1, 4096) == 0 and b(6, 4096) == 0          # one kernel, no scratch
-    assert b(7, 4096) == 7 * 4096 + 28 and b(40, 100) == 40 * 112 + 160
+    assert b(1, 4096) == 0 and b(4, 4096) == 0          # one kernel, no scratch
+    assert b(5, 4096) == 5 * 4096 + 20 and b(40, 100) == 40 * 112 + 160
     assert b(2, 131071) == 2 * 131072 + 8               # codes too large for shared memory
     assert b(-1, 10) == 0 and b(100, 0) == 0
 
