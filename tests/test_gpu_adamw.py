@@ -350,6 +350,34 @@ def test_updated_leaves_are_known_to_autograd():
         y.backward()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_offsets_past_32_bits(bits):
+    n, tail = 2 ** 31 + 2 ** 20 + 77, 2 ** 20 + 77
+    params, grads, states, _ = _make((tail,), bits, BF16, BF16, 14)
+
+    def big(x):          # zeros up to a block's start, then x
+        raw = torch.uint8 if x.dtype == E4M3 else x.dtype
+        y = torch.zeros(n, dtype=raw, device="cuda")
+        y[n - tail:] = x.view(raw)
+        return y.view(x.dtype)
+
+    p, g = big(params[0]), big(grads[0])
+    m, v = big(states[0].m), big(states[0].v)
+    if bits == 8:
+        skip = (n - tail) // 256
+        scales = [torch.cat((torch.zeros(skip, device="cuda"), s)) for s in states[0][2:]]
+        s = rk.AdamWState(m, v, *scales)
+    else:
+        s = rk.AdamWState(m, v)
+    clip, clip_small = rk.relkl_grad_norm([g], 0.1), rk.relkl_grad_norm(grads, 0.1)
+    # the same squares in other partial sums: two roundings
+    assert abs(float(clip[0]) / float(clip_small[0]) - 1) <= 2 * U
+    rk.relkl_adamw([p], [g], [s], step=3, **HYPER)
+    rk.relkl_adamw(params, grads, states, step=3, **HYPER)
+    assert torch.equal(p[n - tail:], params[0]) and not p[:1000].any()
+    assert torch.equal(s.m.view(torch.uint8)[-tail * m.element_size():], states[0].m.view(torch.uint8))
+
+
 def test_other_stream():
     params, grads, states, _ = _make((50000,), 8, F32, F32, 12)
     want = _expect(params, grads, states, 2, 0.1)

@@ -193,6 +193,16 @@ def test_views_strides_and_alignment(rows, dtype, offset):
     assert one.shape == (cols,) and torch.equal(one, y3[0, 0])
 
 
+@pytest.mark.parametrize("cols", [4096, 4097])
+def test_offsets_past_32_bits(cols):
+    rows, K = 2 ** 31 // 4096 + 300, 16              # more than 2^31 results
+    w, sw = _weights(cols, K)
+    x = _randn((rows, K), BF16, 15)
+    y = rk.relkl_linear_i8(x, w, sw)
+    for at in (0, rows - 259):
+        assert torch.equal(y[at:at + 259], rk.relkl_linear_i8(x[at:at + 259], w, sw))
+
+
 def test_no_rows_and_no_channels():
     w, sw = _weights(8, 32)
     assert rk.relkl_linear_i8(torch.empty(0, 32, device="cuda"), w, sw).shape == (0, 8)

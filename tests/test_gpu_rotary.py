@@ -156,6 +156,19 @@ def test_many_heads_and_no_tokens():
     assert rk.relkl_rotary(torch.empty(0, 3, 4, 8, device="cuda"), f, positions=empty).numel() == 0
 
 
+def test_offsets_past_32_bits():
+    far = 2 ** 31 + 64                               # elements between the two batch elements
+    f, _ = rk.rotary_freqs(64)
+    buf = torch.zeros(far + 3 * 5 * 64, dtype=BF16, device="cuda")
+    x = buf.as_strided((2, 3, 5, 64), (far, 5 * 64, 64, 1))
+    small = _randn((2, 3, 5, 64), BF16, 21)
+    x.copy_(small)
+    want = rk.relkl_rotary(small, f)
+    assert torch.equal(rk.relkl_rotary(x, f), want)
+    rk.relkl_rotary(x, f, out=x)
+    assert torch.equal(x, want)
+
+
 def test_special_values_stay_in_their_pair():
     f, _ = rk.rotary_freqs(8)
     x = _randn((1, 1, 3, 16), F32, 7)
