@@ -559,31 +559,49 @@ __device__ __forceinline__ void scaled_words(const float* scales, const float* b
 
 // Rows of y may start anywhere: then a warp turns its 32 rows through shared
 // memory and stores along them, WORDS words of a row to as many lanes.  In
-// bf16 a word is two columns; a row that starts in the middle of a word has
-// them paired with one column's shift.
+// bf16 a word is two columns; where a row starts in the middle of a word they
+// are paired with one column's shift, and its first and last column go alone.
+// Whole blocks, which is most of them, take the short loop: with the edges'
+// conditions in it 30000 x 1024 x 3001 took 157 us.
 template <typename U, int WORDS>
 __device__ __forceinline__ void store_turned(const I8Params& p, const uint32_t* turn, int64_t row0, int c0) {
   const int lane = threadIdx.x & 31, l = lane % WORDS;
-  const int left = p.cols - c0;
+  constexpr int STEP = 32 / WORDS;                 // rows of one store
+  const int left = p.cols - c0, first = lane / WORDS;
   __syncwarp();
-#pragma unroll 8
-  for (int r = lane / WORDS; r < 32; r += 32 / WORDS) {
-    if (row0 + r >= p.rows) break;
-    U* y = static_cast<U*>(p.y) + (row0 + r) * p.y_stride + c0;
-    const uint32_t a = turn[r * TURN_PITCH + l];
+  const uint32_t* from = turn + first * TURN_PITCH + l;
+  U* y = static_cast<U*>(p.y) + (row0 + first) * p.y_stride + c0;
+  if (row0 + 32 <= p.rows && left >= WORDS * static_cast<int>(4 / sizeof(U))) {
+    char* at = reinterpret_cast<char*>(y) + 4 * l;
+    const int64_t step = p.y_stride * STEP * static_cast<int64_t>(sizeof(U));
     if constexpr (sizeof(U) == 4) {
-      if (l < left) y[l] = __uint_as_float(a);
+#pragma unroll 8
+      for (int r = 0; r < 32; r += STEP, at += step)
+        *reinterpret_cast<uint32_t*>(at) = from[r * TURN_PITCH];
     } else {
-      const uint32_t b = turn[r * TURN_PITCH + min(l + 1, WORDS - 1)];
-      unsigned short* h = reinterpret_cast<unsigned short*>(y);
-      const int shift = (reinterpret_cast<uintptr_t>(y) & 2) != 0;   // the same for the row's lanes
-      const uint32_t pair = shift ? (a >> 16) | (b << 16) : a;
-      const int c = 2 * l + shift;
-      if (c + 1 < left && c + 1 < 2 * WORDS)
-        *reinterpret_cast<uint32_t*>(h + c) = pair;
-      else if (c < left)
-        h[c] = static_cast<unsigned short>(pair);
-      if (shift && l == 0) h[0] = static_cast<unsigned short>(a);
+      uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(y) & 2);      // bytes
+      const uint32_t odd = static_cast<uint32_t>(step & 2);
+      const bool edge = l == 0 || l == WORDS - 1;
+#pragma unroll 8
+      for (int r = 0; r < 32; r += STEP, at += step, shift ^= odd) {
+        const uint32_t a = from[r * TURN_PITCH], b = from[r * TURN_PITCH + (l < WORDS - 1)];
+        const uint32_t pair = __byte_perm(a, b, shift ? 0x5432 : 0x3210);
+        if (!shift || l < WORDS - 1) *reinterpret_cast<uint32_t*>(at + shift) = pair;
+        if (shift && edge)
+          *reinterpret_cast<unsigned short*>(at + (l ? 2 : 0)) = static_cast<unsigned short>(l ? a >> 16 : a);
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int r = 0; r < 32 && row0 + first + r < p.rows; r += STEP, y += p.y_stride * STEP) {
+      const uint32_t a = from[r * TURN_PITCH];
+      if constexpr (sizeof(U) == 4) {
+        if (l < left) y[l] = __uint_as_float(a);
+      } else {
+        unsigned short* h = reinterpret_cast<unsigned short*>(y) + 2 * l;
+        if (2 * l < left) h[0] = static_cast<unsigned short>(a);
+        if (2 * l + 1 < left) h[1] = static_cast<unsigned short>(a >> 16);
+      }
     }
   }
   __syncwarp();     // read before the next block is written
