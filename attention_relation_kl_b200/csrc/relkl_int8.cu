@@ -1108,7 +1108,20 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
           continue;
         }
         // boxes of 32 rows x 128 bytes, swizzled against bank conflicts, go to
-        // y by TMA: whole lines, and what lies past the edges is left out
+        // y by TMA: whole lines, and what lies past the edges is left out, but
+        // only in units of 16 bytes; the columns of a last, partial unit are
+        // stored by themselves
+        if (p.box_cols < p.cols && c + 32 > p.box_cols && row < p.rows) {
+          U* y = static_cast<U*>(p.y) + row * p.y_stride + c;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c + j >= p.box_cols && c + j < p.cols) {
+              if constexpr (sizeof(U) == 4)
+                y[j] = __uint_as_float(w[j]);
+              else
+                reinterpret_cast<unsigned short*>(y)[j] = static_cast<unsigned short>(w[j / 2] >> (16 * (j & 1)));
+            }
+        }
         if (part == 0) {
           if (lane == 0) bulk_wait_read<0>();                   // the last box has been read
           __syncwarp();
@@ -1122,7 +1135,7 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
           __syncwarp();
           const int64_t r_box = row - lane;
           if (lane == 0) {
-            if (c_box < p.cols && r_box < p.rows) tma_store_2d(&p.tm_y, box, c_box, static_cast<int>(r_box));
+            if (c_box < p.box_cols && r_box < p.rows) tma_store_2d(&p.tm_y, box, c_box, static_cast<int>(r_box));
             bulk_commit();
           }
         }
@@ -1196,10 +1209,10 @@ bool encode_codes(CUtensorMap* m, const int8_t* q, int64_t rows, int K, int64_t 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// y as boxes of 32 rows x 128 bytes
+// y's first box_cols columns as boxes of 32 rows x 128 bytes
 template <typename U>
 bool encode_out(CUtensorMap* m, const I8Params& p, EncodeTiled encode) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.cols), static_cast<cuuint64_t>(p.rows)};
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.box_cols), static_cast<cuuint64_t>(p.rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.y_stride) * sizeof(U)};
   const cuuint32_t boxes[2] = {128 / sizeof(U), 32}, ones[2] = {1, 1};
   return encode(m, sizeof(U) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.y,
@@ -1251,6 +1264,9 @@ template <int BN, typename U>
 cudaError_t gemm_pair(I8Params& p, const I8Call& c, int num_sms, cudaStream_t stream) {
   using S = i8::PairSmem<BN>;
   const int64_t m = (p.rows + 2 * i8::BM - 1) / (2 * i8::BM), n = (p.cols + BN - 1) / BN;
+  constexpr int unit = 16 / sizeof(U);             // columns of 16 bytes
+  p.box_cols = p.cols / unit * unit;
+  if (p.box_cols == 0) p.y_wide = 0;
   if (!encode_codes(&p.tm_a, c.q, p.rows, c.K, c.q_stride, i8::BM, c.encode) ||
       !encode_codes(&p.tm_b, c.w, p.cols, c.K, c.w_stride, BN / 2, c.encode) ||
       (p.y_wide && !encode_out<U>(&p.tm_y, p, c.encode)))

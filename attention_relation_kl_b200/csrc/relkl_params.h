@@ -190,7 +190,7 @@ struct GemvParams {
 struct I8Params {
   CUtensorMap tm_a;                   // codes [rows, K]: box 128 bytes x up to 128 rows, 128B swizzle
   CUtensorMap tm_b;                   // weights [cols, K]: box 128 bytes x BN rows
-  CUtensorMap tm_y;                   // y: box 128 bytes x 32 rows, 128B swizzle (pairs, y_wide)
+  CUtensorMap tm_y;                   // y [rows, box_cols]: box 128 bytes x 32 rows, 128B swizzle (pairs, y_wide)
   const float *x_scale, *w_scale, *bias;
   void* y;
   int64_t rows, y_stride;
@@ -198,6 +198,7 @@ struct I8Params {
   int y_wide;                         // rows of y start at 16-byte (1) or 32-byte (2) boundaries
   int m_tiles, n_tiles, n_units, k_chunks, split;   // set by the launch
   int a_box;                          // rows of tm_a's box (one CTA for a tile)
+  int box_cols;                       // columns of tm_y: cols, down to whole 16 bytes (pairs)
   DevStatus* status;
   unsigned long long timeout_ns;
 };

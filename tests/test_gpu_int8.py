@@ -193,6 +193,21 @@ def test_views_strides_and_alignment(rows, dtype, offset):
     assert one.shape == (cols,) and torch.equal(one, y3[0, 0])
 
 
+# rows of y that start at 16-byte boundaries and end anywhere, in every kernel
+@pytest.mark.parametrize("yt", [BF16, F32])
+@pytest.mark.parametrize("rows", [3, 40, 300, 600, 5000])
+@pytest.mark.parametrize("cols", [3, 993, 1001, 1002, 1004, 1007, 1008])
+def test_nothing_is_written_beside_a_wide_output(cols, rows, yt):
+    x = _randn((rows, 64), BF16, 16)
+    w, sw = _weights(cols, 64)
+    buf = torch.full((rows + 2, (cols + 15) // 8 * 8), 7.0, dtype=yt, device="cuda")
+    rk.relkl_linear_i8(x, w, sw, out_dtype=yt, out=buf[1:-1, :cols])
+    assert torch.equal(buf[1:-1, :cols], rk.relkl_linear_i8(x, w, sw, out_dtype=yt))
+    _check(buf[1:-1, :cols], *_codes(x), w, sw)
+    buf[1:-1, :cols] = 7.0
+    assert (buf == 7.0).all()
+
+
 @pytest.mark.parametrize("cols", [4096, 4097])
 def test_offsets_past_32_bits(cols):
     rows, K = 2 ** 31 // 4096 + 300, 16              # more than 2^31 results
