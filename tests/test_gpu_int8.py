@@ -208,6 +208,24 @@ def test_nothing_is_written_beside_a_wide_output(cols, rows, yt):
     assert (buf == 7.0).all()
 
 
+@pytest.mark.parametrize("rows", [2, 40, 300, 600, 5000])
+@pytest.mark.parametrize("K", [1, 5, 15, 17, 31, 100, 130, 1001])
+def test_what_lies_behind_the_rows_of_codes_is_not_read(K, rows):
+    cols, pitch = 1000, (K + 31) // 16 * 16
+
+    def padded(q):
+        wide = torch.full((q.shape[0], pitch), 99, dtype=torch.int8, device="cuda")
+        wide[:, :K] = q
+        return wide[:, :K]
+
+    x = _randn((rows, K), BF16, 17)
+    w, sw = _weights(cols, K)
+    q, s = rk.relkl_quantize_rows(x)
+    want = rk.relkl_matmul_i8(padded(q), s, padded(w), sw, out_dtype=F32)
+    _check(want, *_codes(x), w, sw)
+    assert torch.equal(rk.relkl_linear_i8(x, padded(w), sw, out_dtype=F32), want)
+
+
 @pytest.mark.parametrize("cols", [4096, 4097])
 def test_offsets_past_32_bits(cols):
     rows, K = 2 ** 31 // 4096 + 300, 16              # more than 2^31 results
