@@ -84,7 +84,9 @@ struct RotaryTensor {
   int64_t xs[3], ys[3];      // element strides of B, H, N
   int H;
   int apply;                 // 0: moved and converted only
-  int groups;                // head groups (set by the launch)
+  // set by the launch: head groups; a thread's parts of a head, the first
+  // rot_chunks of them rotated, the others `width` entries each
+  int groups, chunks, rot_chunks, width;
 };
 
 struct RotaryParams {
@@ -99,8 +101,8 @@ struct RotaryParams {
   float mscale;
   double pos_scale, pos_offset;
   // set by the launch
-  int chunks, rot_chunks, heads_per_group;
-  int64_t n_items;
+  int heads_per_group;
+  int64_t tokens;
 };
 
 // AdamW: tables of tensors travel in the kernel's parameters (32,764 bytes at

@@ -120,43 +120,49 @@ __device__ __forceinline__ void move_heads(const T* x, U* y, int64_t xh, int64_t
   }
 }
 
+// The entries that do not turn, or a tensor that does not: `width` of them to
+// a thread, whatever the rotated part's width is.
+template <typename T, typename U>
+__device__ __forceinline__ void move_chunk(const T* x, U* y, int64_t xh, int64_t yh, int heads, int width) {
+  switch (width) {
+    case 8: move_heads<T, U, 8>(x, y, xh, yh, heads); break;
+    case 4: move_heads<T, U, 4>(x, y, xh, yh, heads); break;
+    case 2: move_heads<T, U, 2>(x, y, xh, yh, heads); break;
+    default: move_heads<T, U, 1>(x, y, xh, yh, heads);
+  }
+}
+
 }  // namespace
 
 // Thread = (token, chunk): a chunk is V pairs of the `half` layout (V entries
 // of each half), V / 2 pairs of the interleaved layout (V neighbouring
-// entries; with V = 1 one pair, entry by entry), or V entries behind the
-// rotated part.  blockIdx.y = head group.
+// entries; with V = 1 one pair, entry by entry), or some entries that do not
+// turn.  blockIdx.y = head group of a tensor.
 template <typename T, typename U, int V, bool HALVES>
 __global__ void __launch_bounds__(256, 8) relkl_rotary_kernel(const __grid_constant__ RotaryParams p) {
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (item >= p.n_items) return;
-  const int64_t tok = item / p.chunks;
-  const int chunk = static_cast<int>(item - tok * p.chunks);
-  const int64_t b = tok / p.N, n = tok - b * p.N;
-
   // the group's tensor and first head
   int g = blockIdx.y, r = 0;
   while (g >= p.t[r].groups) g -= p.t[r++].groups;
   const RotaryTensor& t = p.t[r];
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t tok = item / t.chunks;
+  const int chunk = static_cast<int>(item - tok * t.chunks);
+  if (tok >= p.tokens) return;
+  const int64_t b = tok / p.N, n = tok - b * p.N;
   const int h0 = g * p.heads_per_group;
   const int heads = min(p.heads_per_group, t.H - h0);
   const T* x = static_cast<const T*>(t.x) + b * t.xs[0] + h0 * t.xs[1] + n * t.xs[2];
   U* y = static_cast<U*>(t.y) + b * t.ys[0] + h0 * t.ys[1] + n * t.ys[2];
   const int64_t xh = t.xs[1], yh = t.ys[1];
 
-  if (chunk >= p.rot_chunks) {   // behind the rotated part
-    const int at = p.rot + (chunk - p.rot_chunks) * V;
-    move_heads<T, U, V>(x + at, y + at, xh, yh, heads);
+  if (chunk >= t.rot_chunks) {
+    const int at = (t.apply ? p.rot : 0) + (chunk - t.rot_chunks) * t.width;
+    move_chunk<T, U>(x + at, y + at, xh, yh, heads, t.width);
     return;
   }
   constexpr bool SPLIT = HALVES || V == 1;   // a pair's entries are loaded apart
   const int at = (!HALVES && V == 1) ? 2 * chunk : chunk * V;
   const int far = HALVES ? p.rot / 2 : 1;
-  if (!t.apply) {
-    move_heads<T, U, V>(x + at, y + at, xh, yh, heads);
-    if constexpr (SPLIT) move_heads<T, U, V>(x + at + far, y + at + far, xh, yh, heads);
-    return;
-  }
 
   double pos;
   if (p.positions) {
@@ -218,22 +224,45 @@ __global__ void __launch_bounds__(256, 8) relkl_rotary_kernel(const __grid_const
 
 namespace {
 
+// Largest of 8, 4, 2, 1, at most `most`, that divides `entries` and whose
+// accesses, of at most 16 bytes, are aligned at entry `at` of every head.  The
+// rotated parts of a launch share one width, whatever does not turn has its
+// own: 8192 tokens of 32 + 8 + 8 heads in bf16 took, with one width for all,
+// 40.5 (40 of 80 entries turn), 55.1 (24 of 96) and 96.5 us (20 of 128), and
+// take 29.9, 37.8 and 60.6; where all of a head turns, 41.6 and 39.7.
+int vector_width(const RotaryTensor& t, int most, int at, int entries, int xsize, int ysize) {
+  for (int v = most; v > 1; v /= 2) {
+    const int64_t xa = v * xsize < 16 ? v * xsize : 16, ya = v * ysize < 16 ? v * ysize : 16;
+    bool ok = entries % v == 0 && at * xsize % xa == 0 && at * ysize % ya == 0 &&
+              reinterpret_cast<uintptr_t>(t.x) % xa == 0 && reinterpret_cast<uintptr_t>(t.y) % ya == 0;
+    for (int i = 0; i < 3; ++i) ok = ok && t.xs[i] * xsize % xa == 0 && t.ys[i] * ysize % ya == 0;
+    if (ok) return v;
+  }
+  return 1;
+}
+
 template <typename T, typename U, int V, bool HALVES>
 cudaError_t launch(RotaryParams& p, int num_sms, cudaStream_t stream) {
-  p.rot_chunks = (HALVES || V == 1) ? p.rot / 2 / V : p.rot / V;
-  p.chunks = p.rot_chunks + (p.d - p.rot) / V;
-  p.n_items = static_cast<int64_t>(p.B) * p.N * p.chunks;
-  const int64_t blocks = (p.n_items + 255) / 256;
+  p.tokens = static_cast<int64_t>(p.B) * p.N;
+  int64_t blocks = 0;
+  int most = 1;
+  int64_t work = 0;     // blocks with one head to a thread
+  for (int r = 0; r < p.n; ++r) {
+    RotaryTensor& t = p.t[r];
+    const int turned = t.apply ? p.rot : 0;
+    t.rot_chunks = (HALVES || V == 1) ? turned / 2 / V : turned / V;
+    t.width = vector_width(t, (sizeof(T) == 2 && sizeof(U) == 2) ? 8 : 4, turned, p.d - turned, sizeof(T), sizeof(U));
+    t.chunks = t.rot_chunks + (p.d - turned) / t.width;
+    const int64_t own = (p.tokens * t.chunks + 255) / 256;
+    blocks = own > blocks ? own : blocks;
+    work += own * t.H;
+    most = t.H > most ? t.H : most;
+  }
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   // As many heads for one thread as leave the SMs two waves of blocks, but at
   // most 4: with 1, 2, 4, 8, 16 heads the 32K inputs took 493, 319, 279, 285,
   // 289 us (angles weigh on the left, distant rows in flight on the right).
-  int most = 1, all = 0;
-  for (int r = 0; r < p.n; ++r) {
-    most = p.t[r].H > most ? p.t[r].H : most;
-    all += p.t[r].H;
-  }
-  int64_t hg = blocks * all / (static_cast<int64_t>(num_sms) * 16);
+  int64_t hg = work / (static_cast<int64_t>(num_sms) * 16);
   hg = hg < 1 ? 1 : (hg > 4 ? 4 : hg);
   while ((most + hg - 1) / hg * p.n > 65535) hg *= 2;   // the grid's y extent
   p.heads_per_group = static_cast<int>(hg);
@@ -247,29 +276,13 @@ cudaError_t launch(RotaryParams& p, int num_sms, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// Largest V <= most (a power of two) that divides the parts of a head and
-// whose accesses are aligned: V * size bytes, at most 16, at every head's start.
-int vector_width(const RotaryParams& p, int most, int xsize, int ysize, bool halves) {
-  for (int v = most; v > 1; v /= 2) {
-    if ((p.d - p.rot) % v || (halves ? (p.rot / 2) % v : p.rot % v)) continue;
-    const int64_t xa = v * xsize < 16 ? v * xsize : 16, ya = v * ysize < 16 ? v * ysize : 16;
-    bool ok = true;
-    for (int r = 0; r < p.n && ok; ++r) {
-      ok = reinterpret_cast<uintptr_t>(p.t[r].x) % xa == 0 &&
-           reinterpret_cast<uintptr_t>(p.t[r].y) % ya == 0;
-      for (int i = 0; i < 3; ++i)
-        ok = ok && p.t[r].xs[i] * xsize % xa == 0 && p.t[r].ys[i] * ysize % ya == 0;
-    }
-    if (ok) return v;
-  }
-  return 1;
-}
-
 template <typename T, typename U, bool HALVES>
 cudaError_t pick(RotaryParams& p, int num_sms, cudaStream_t stream) {
   // 16 bytes of the wider type in one access
   constexpr int most = (sizeof(T) == 2 && sizeof(U) == 2) ? 8 : 4;
-  const int v = vector_width(p, most, sizeof(T), sizeof(U), HALVES);
+  int v = most;
+  for (int r = 0; r < p.n; ++r)
+    if (p.t[r].apply) v = vector_width(p.t[r], v, 0, HALVES ? p.rot / 2 : p.rot, sizeof(T), sizeof(U));
   if constexpr (most == 8)
     if (v == 8) return launch<T, U, 8, HALVES>(p, num_sms, stream);
   if (v == 4) return launch<T, U, 4, HALVES>(p, num_sms, stream);

@@ -264,3 +264,29 @@ def test_bad_calls_are_refused():
         rk.relkl_rotary(x, f, out_dtype=torch.float16)
     with pytest.raises(RuntimeError):
         rk.relkl_rotary(x, f, out=x[:, :, :1].expand(1, 2, 4, 64))
+
+
+# each tensor of a launch is read in accesses of its own width: a rotated or a moved one
+# whose rows start anywhere leaves the others', and the rest of a head, as they should be
+@pytest.mark.parametrize("odd", [0, 1, 2])
+@pytest.mark.parametrize("apply", [(True, False, True), (False, False, False)])
+@pytest.mark.parametrize("xt,yt", [(BF16, BF16), (BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("d,rot", [(64, 4), (64, 62), (48, 16), (128, 20)])
+def test_tensors_of_different_alignment_in_one_launch(d, rot, xt, yt, apply, odd):
+    B, N = 2, 19
+    xs, outs = [], []
+    for i, h in enumerate((5, 1, 3)):
+        shift = 1 if i == odd else 0
+        xs.append(_randn((B * h * N * d + shift,), xt, i)[shift:].view(B, h, N, d))
+        outs.append(torch.full((B * h * N * d + shift,), 7.0, dtype=yt, device="cuda")[shift:].view(B, h, N, d))
+    f, _ = rk.rotary_freqs(rot)
+    pos = _positions(None, B, N)
+    for interleaved in (False, True):
+        rk.relkl_rotary_qkv(xs, f, apply=apply, interleaved=interleaved, out=outs)
+        for x, y, turns in zip(xs, outs, apply):
+            if turns:
+                want, err = _reference(x, f, pos, 1.0, interleaved, False)
+                _check(y[..., :rot], want[..., :rot], err[..., :rot])
+                assert torch.equal(y[..., rot:], x[..., rot:].to(yt))
+            else:
+                assert torch.equal(y, x.to(yt))
