@@ -6,9 +6,13 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <unordered_set>
 #include <vector>
 
+#include <c10/core/impl/VirtualGuardImpl.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 
 #include "../../include/relkl.h"
 
@@ -187,6 +191,28 @@ PyObject* written(PyObject*, PyObject* arg) {
       if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
     }
     Py_RETURN_NONE;
+  });
+}
+
+// graph_elsewhere(x) -> whether a node that x's gradient would reach belongs to another stream
+// of x's device than the current one
+PyObject* graph_elsewhere(PyObject*, PyObject* arg) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& x = tensor(arg, "x");
+    if (!x.is_cuda() || !x.requires_grad()) Py_RETURN_FALSE;
+    const c10::Stream here = c10::impl::VirtualGuardImpl(c10::DeviceType::CUDA).getStream(x.device());
+    std::unordered_set<torch::autograd::Node*> seen;
+    const auto edge = torch::autograd::impl::gradient_edge(x);
+    std::vector<torch::autograd::Node*> next{edge.function.get()};
+    while (!next.empty()) {
+      torch::autograd::Node* node = next.back();
+      next.pop_back();
+      if (!node || !seen.insert(node).second) continue;
+      const auto stream = node->stream();
+      if (stream && stream->device() == here.device() && *stream != here) Py_RETURN_TRUE;
+      for (const auto& e : node->next_edges()) next.push_back(e.function.get());
+    }
+    Py_RETURN_FALSE;
   });
 }
 
@@ -402,6 +428,7 @@ PyObject* vector(PyObject*, PyObject* args) {
 PyMethodDef methods[] = {
     {"adamw", adamw, METH_VARARGS, "records of relkl_adamw"},
     {"written", written, METH_O, "marks tensors as changed in place"},
+    {"graph_elsewhere", graph_elsewhere, METH_O, "whether a gradient would leave the current stream"},
     {"norm", norm, METH_O, "records of relkl_grad_norm"},
     {"rotary_inputs", rotary_inputs, METH_VARARGS, "checks of relkl_rotary's inputs"},
     {"rotary", rotary, METH_VARARGS, "records of relkl_rotary"},

@@ -97,6 +97,8 @@ def relkl_matmul_i8(q: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, w_s
         check(_abi.lib().relkl_matmul_i8(rows, cols, K, q_ptr, q_stride, qs, w_ptr, w_stride, s, b,
                                          y_ptr, y_type, y_stride, ws.data_ptr(), ws.numel(), handle),
               "relkl_matmul_i8")
+    if out is not None:
+        m.written([out])
     return y
 
 
@@ -128,4 +130,6 @@ def relkl_linear_i8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
         check(lib.relkl_linear_i8(rows, cols, K, x_ptr, x_type, stride, w_ptr, w_stride, s, b, y_ptr,
                                   y_type, y_stride, None if scratch is None else scratch.data_ptr(),
                                   nbytes, ws.data_ptr(), ws.numel(), handle), "relkl_linear_i8")
+    if out is not None:
+        m.written([out])
     return y

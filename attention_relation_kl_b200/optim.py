@@ -108,6 +108,7 @@ def relkl_grad_norm(grads: Sequence[torch.Tensor], max_norm: float = math.inf, *
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
         check(lib.relkl_grad_norm(n, table, max_norm, out.data_ptr(), scratch.data_ptr(), nbytes,
                                   handle), "relkl_grad_norm")
+    _abi.marshal().written([out])
     return out
 
 

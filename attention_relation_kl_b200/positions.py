@@ -103,13 +103,13 @@ def relkl_rotary_qkv(xs: Sequence[torch.Tensor], inv_freq: torch.Tensor, *,
     elif out_dtype is not None and any(y.dtype != out_dtype for y in out):
         raise ValueError(f"out must be {out_dtype} tensors")
     with _on(x0.device, stream) as handle:
-        if out is None:
-            out = [torch.empty(x.shape, dtype=out_dtype, device=x0.device) for x in xs]
-        else:
-            out = list(out)
+        given = out is not None
+        out = list(out) if given else [torch.empty(x.shape, dtype=out_dtype, device=x0.device) for x in xs]
         tensors, plan = marshal.rotary(xs, out, apply, inv_freq, positions, interleaved, inverse,
                                        mscale, pos_scale, pos_offset)
         check(_abi.lib().relkl_rotary(len(out), tensors, plan, handle), "relkl_rotary")
+    if given:
+        marshal.written(out)
     return out
 
 
@@ -132,10 +132,16 @@ class Rotary(torch.autograd.Function):
     def forward(ctx, x, inv_freq, positions, args, out_dtype):
         ctx.save_for_backward(inv_freq, positions)
         ctx.args, ctx.dtype = args, x.dtype
+        ctx.elsewhere = (x.requires_grad and x.is_cuda and torch.cuda.is_current_stream_capturing()
+                         and _abi.marshal().graph_elsewhere(x))
         return relkl_rotary(x.detach(), inv_freq, positions=positions, out_dtype=out_dtype, **args)
 
     @staticmethod
     def backward(ctx, dy):
+        # autograd would make that stream wait for the captured one, which ends the process
+        if ctx.elsewhere and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a leaf of this graph belongs to an eager graph on another stream: drop "
+                               "that graph before capturing a backward pass")
         inv_freq, positions = ctx.saved_tensors
         if dy.dim() and dy.stride(-1) != 1:
             dy = dy.contiguous()
@@ -148,7 +154,10 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, *, positions: Optional[torch
            pos_scale: float = 1.0, pos_offset: float = 0.0, mscale: float = 1.0,
            interleaved: bool = False, inverse: bool = False,
            out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
-    """Differentiable relkl_rotary (the frequencies and positions get no gradient)."""
+    """Differentiable relkl_rotary (the frequencies and positions get no gradient).
+
+    Its backward pass may be captured into a graph once no eager graph of the same leaves,
+    made on another stream, is alive; until then it is refused."""
     args = dict(pos_scale=pos_scale, pos_offset=pos_offset, mscale=mscale, interleaved=interleaved,
                 inverse=bool(inverse))
     return Rotary.apply(x, inv_freq, positions, args, out_dtype)

@@ -324,3 +324,16 @@ def test_bad_calls_are_refused():
             call()
     with pytest.raises(RuntimeError):
         rk.relkl_quantize_rows(torch.zeros(2, 131072, device="cuda"))
+
+
+def test_given_outputs_are_seen_as_changed_in_place():
+    x, w = torch.randn(5, 64, device="cuda"), torch.randn(48, 64, device="cuda")
+    (q, s), (qw, sw) = rk.relkl_quantize_rows(x), rk.relkl_quantize_rows(w)
+    for call in (lambda out: rk.relkl_linear_i8(x, qw, sw, out=out),
+                 lambda out: rk.relkl_matmul_i8(q, s, qw, sw, out=out, out_dtype=torch.float32)):
+        out = torch.ones(5, 48, device="cuda")
+        a = torch.zeros_like(out, requires_grad=True)
+        y = (a * out).sum()
+        call(out)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()

@@ -290,3 +290,35 @@ def test_tensors_of_different_alignment_in_one_launch(d, rot, xt, yt, apply, odd
                 assert torch.equal(y[..., rot:], x[..., rot:].to(yt))
             else:
                 assert torch.equal(y, x.to(yt))
+
+
+def test_captured_backward_pass():
+    x = _randn((1, 3, 17, 64), F32, 1).requires_grad_()
+    w = _randn((1, 3, 17, 64), F32, 2)
+    f, _ = rk.rotary_freqs(64)
+    eager = rk.rotary(x, f)
+    # x's gradient node belongs to the eager graph's stream: refused, and nothing is lost
+    with pytest.raises(RuntimeError, match="eager graph"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            z = rk.rotary(x * 1.0, f)
+            torch.autograd.grad(z, x, w)
+    del z
+    (want,) = torch.autograd.grad(eager, x, w)
+    del eager
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        z = rk.rotary(x * 1.0, f)
+        (got,) = torch.autograd.grad(z, x, w)
+    for _ in range(2):
+        got.zero_()
+        graph.replay()
+        assert torch.equal(got, want)
+
+
+def test_given_outputs_are_seen_as_changed_in_place():
+    x, f = _randn((1, 2, 5, 64), F32), rk.rotary_freqs(64).inv_freq
+    a = torch.zeros_like(x, requires_grad=True)
+    y = (a * x).sum()                     # x is saved for a's gradient
+    rk.relkl_rotary(x, f, out=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
