@@ -404,12 +404,19 @@ __global__ void __launch_bounds__(THREADS, 8) relkl_adamw_kernel(const __grid_co
 }
 
 // ------------------------------------------------------- gradient norm
-// sqrt(sum of g^2) over all tensors.  Eight squares are summed in float32, the
-// rest in double precision, in an order that depends on the sizes and the
-// grid only, so the same gradients give the same bits.
+// sqrt(sum of g^2) over all tensors.  Eight squares are summed in float32, or
+// where that leaves float32's range in double precision, as is the rest, in an
+// order that depends on the sizes and the grid only, so the same gradients
+// give the same bits.  An element from 2^64 on, whose square float32 does not
+// hold, counts as infinite: such a step is left out by its clipping factor.
 namespace {
 
 constexpr int NORM_CHUNK = 8192;
+constexpr float NORM_MOST = 0x1p64f;
+
+__device__ __forceinline__ double square(float x) {
+  return fabsf(x) < NORM_MOST ? static_cast<double>(x) * x : static_cast<double>(x * x);
+}
 
 template <typename G>
 __device__ double chunk_squares(const NormTensor& t, int64_t begin) {
@@ -425,11 +432,19 @@ __device__ double chunk_squares(const NormTensor& t, int64_t begin) {
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) s = fmaf(x[k], x[k], s);
-    sum += s;
+    if (s >= 1e-30f && isfinite(s)) {
+      sum += s;
+      continue;
+    }
+    float most = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) most = larger(most, x[k]);
+    if (most == 0.0f) continue;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += square(x[k]);
   }
   for (int64_t i = wide + threadIdx.x; i < end; i += blockDim.x) {
-    const float x = load1(g + i);
-    sum += static_cast<double>(x) * x;
+    sum += square(load1(g + i));
   }
   return sum;
 }

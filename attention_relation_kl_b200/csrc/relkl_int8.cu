@@ -449,7 +449,9 @@ __device__ __forceinline__ void mma_lead(uint32_t leader, uint32_t d_tmem, uint3
 }
 
 // Waits for the kernel before this one where this one was started ahead of its
-// end (the coding of the rows; elsewhere it returns at once).
+// end (the coding of the rows; elsewhere it returns at once).  What that kernel
+// writes is read past the read-only cache, which takes its data as constant for
+// a kernel's whole time.
 __device__ __forceinline__ void rows_are_coded() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -740,7 +742,7 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
   const int64_t row = static_cast<int64_t>(mt) * BM + q * 32 + lane;
   const bool live = warp >= 2 && row < p.rows;
   if (warp >= 2) rows_are_coded();
-  const float sx = live ? p.x_scale[row] : 0.0f;
+  const float sx = live ? __ldcg(p.x_scale + row) : 0.0f;
   uint32_t* turn = reinterpret_cast<uint32_t*>(gbase + S::TURN + (warp & 3) * TURN_BYTES);
   float* scales = reinterpret_cast<float*>(gbase + S::SCALES) + (warp & 3) * 2 * BN;
   if (warp >= 2) {
@@ -1070,7 +1072,7 @@ relkl_gemm_i8_pair_kernel(const __grid_constant__ I8Params p) {
       pair_unit(p, unit, mt, nt);
       row_next = static_cast<int64_t>(mt) * 2 * BM + rank * BM + q * 32 + lane;
       col_next = nt * BN + half;
-      sx_next = row_next < p.rows ? __ldg(p.x_scale + row_next) : 0.0f;
+      sx_next = row_next < p.rows ? __ldcg(p.x_scale + row_next) : 0.0f;
       columns.fetch(p, col_next);
     };
     if (first < p.n_units) fetch(first);

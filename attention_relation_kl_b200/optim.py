@@ -92,7 +92,8 @@ def relkl_grad_norm(grads: Sequence[torch.Tensor], max_norm: float = math.inf, *
                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Two float32 numbers on the device: the norm of all gradients (bf16 or float32) taken
     together, and the factor min(1, max_norm / (norm + 1e-6)) that clips them to
-    ``max_norm`` (NaN where the norm is not finite), for relkl_adamw's ``grad_scale``."""
+    ``max_norm`` (NaN where the norm is not finite, as with an element from 2^64 on), for
+    relkl_adamw's ``grad_scale``."""
     n = len(grads)
     index, table = _abi.marshal().norm(grads)
     device = grads[0].device

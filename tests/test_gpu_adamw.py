@@ -421,3 +421,28 @@ def test_bad_calls_are_refused():
         rk.relkl_grad_norm([])
     with pytest.raises(ValueError):
         rk.relkl_grad_norm(g, out=torch.empty(3, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("sizes", [(37,), (8192, 100), (300000, 5)])
+def test_norm_whose_squares_leave_float32(sizes, dtype):
+    gen = torch.Generator().manual_seed(12)
+    for powers in ((18,), (-24,), (-35, -20), (18, -30), (0, -24)):
+        for offset in (0, 1):
+            grads = []
+            for k, n in enumerate(sizes):
+                g = torch.randn(n + offset, generator=gen) * 10.0 ** powers[k % len(powers)]
+                g[offset::3] = 0.0
+                grads.append(g.to(dtype).cuda()[offset:])
+            got = rk.relkl_grad_norm(grads)
+            want = math.sqrt(sum(float((_f64(g) ** 2).sum()) for g in grads))
+            # as in range: 8 u of eight squares, halved by the root, and the result's rounding
+            assert abs(float(got[0]) - want) <= 6 * U * want and float(got[1]) == 1.0
+        # an element from 2^64 on counts as infinite, wherever it stands
+        for at in (0, sizes[0] - 1):
+            for x in (2.0 ** 64, -2.0 ** 64):
+                grads[0][at] = x
+                assert float(rk.relkl_grad_norm(grads)[0]) == math.inf
+            grads[0][at] = 2.0 ** 63
+        got, want = rk.relkl_grad_norm(grads), math.sqrt(sum(float((_f64(g) ** 2).sum()) for g in grads))
+        assert abs(float(got[0]) - want) <= 6 * U * want
