@@ -19,11 +19,12 @@
 // statistics of an 8-bit block stay in the registers of its warp.
 //
 // Measured (B200, copy bandwidth 6.56 TB/s), 201 M float32 weights with bf16
-// copies: float32 states 876 us, 6.9 TB/s; 8-bit states 584 us, 6.2 TB/s.  The
-// 8-bit step is close to the issue rate too: with correctly rounded roots and
-// quotients (99 instructions an element) it took 693 us, with two or more
-// blocks for a warp 250 us more (the second block's loads wait for the first's
-// stores), with 256 threads a CTA 594 us.
+// copies and gradients: float32 states 823 us, 6.8 TB/s; 8-bit states 549 us, 5.9
+// TB/s (569 us where a lane's eight elements were neighbours, so that each access
+// touched half of its sectors); bf16 weights without copies 498 us.  The 8-bit step is close to the issue rate too:
+// with correctly rounded roots and quotients (99 instructions an element) it took
+// 693 us, with two or more blocks for a warp 250 us more (the second block's loads
+// wait for the first's stores).
 #include <cmath>
 #include <cstdint>
 
@@ -252,9 +253,9 @@ __device__ __forceinline__ float moved_fast(const Hyper& h, float p, float m, fl
   return fmaf(p, h.decay, -h.step * (m * inv));
 }
 
-// One warp, one block of 256: lane l holds elements 8l .. 8l + 7 in wide
-// accesses, or l, l + 32, ... (the last block, and tensors that are not
-// aligned for wide ones).
+// One warp, one block of 256: lane l holds elements 4l .. 4l + 3 of each half
+// in wide accesses, so that each covers whole sectors, or l, l + 32, ... (the
+// last block, and tensors that are not aligned for wide ones).
 template <typename G, typename P, bool WIDE>
 __device__ __forceinline__ void block8(const AdamwTensor& t, const Hyper& h, int64_t blk) {
   const int lane = threadIdx.x & 31;
@@ -265,19 +266,22 @@ __device__ __forceinline__ void block8(const AdamwTensor& t, const Hyper& h, int
   __nv_bfloat16* c = t.copy ? static_cast<__nv_bfloat16*>(t.copy) + first : nullptr;
   const int left = static_cast<int>(min(t.n - first, static_cast<int64_t>(BLOCK8)));
   float gg[8], pp[8], mm[8], rr[8], vv[8];
-  const int at = 8 * lane;
+  const int at = 4 * lane;
   const float ms = __ldcg(t.m_scale + blk), rs = __ldcg(t.v_scale + blk);
   if constexpr (WIDE) {
-    const uint2 mq = __ldcg(reinterpret_cast<const uint2*>(mc + at));
-    const uint2 rq = __ldcg(reinterpret_cast<const uint2*>(rc + at));
-    load4(g + at, gg);
-    load4(g + at + 4, gg + 4);
-    load4(p + at, pp);
-    load4(p + at + 4, pp + 4);
-    decode4(mq.x, mm);
-    decode4(mq.y, mm + 4);
-    decode4(rq.x, rr);
-    decode4(rq.y, rr + 4);
+    uint32_t mq[2], rq[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      mq[k] = __ldcg(reinterpret_cast<const uint32_t*>(mc + at + 128 * k));
+      rq[k] = __ldcg(reinterpret_cast<const uint32_t*>(rc + at + 128 * k));
+      load4(g + at + 128 * k, gg + 4 * k);
+      load4(p + at + 128 * k, pp + 4 * k);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      decode4(mq[k], mm + 4 * k);
+      decode4(rq[k], rr + 4 * k);
+    }
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -305,10 +309,10 @@ __device__ __forceinline__ void block8(const AdamwTensor& t, const Hyper& h, int
   }
   if constexpr (WIDE) {
     store4(p + at, pp);
-    store4(p + at + 4, pp + 4);
+    store4(p + at + 128, pp + 4);
     if (c) {
       store4(c + at, pp);
-      store4(c + at + 4, pp + 4);
+      store4(c + at + 128, pp + 4);
     }
   } else {
 #pragma unroll
@@ -337,8 +341,10 @@ __device__ __forceinline__ void block8(const AdamwTensor& t, const Hyper& h, int
     rq = make_uint2(encode4(rr), encode4(rr + 4));
   }
   if constexpr (WIDE) {
-    __stcg(reinterpret_cast<uint2*>(mc + at), mq);
-    __stcg(reinterpret_cast<uint2*>(rc + at), rq);
+    __stcg(reinterpret_cast<uint32_t*>(mc + at), mq.x);
+    __stcg(reinterpret_cast<uint32_t*>(mc + at + 128), mq.y);
+    __stcg(reinterpret_cast<uint32_t*>(rc + at), rq.x);
+    __stcg(reinterpret_cast<uint32_t*>(rc + at + 128), rq.y);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -404,48 +410,97 @@ __global__ void __launch_bounds__(THREADS, 8) relkl_adamw_kernel(const __grid_co
 }
 
 // ------------------------------------------------------- gradient norm
-// sqrt(sum of g^2) over all tensors.  Eight squares are summed in float32, or
-// where that leaves float32's range in double precision, as is the rest, in an
-// order that depends on the sizes and the grid only, so the same gradients
+// sqrt(sum of g^2) over all tensors.  The squares of 16 bytes are summed in
+// float32, or where that leaves float32's range in double precision, as is the
+// rest, in an order that depends on the sizes and the grid only, so the same gradients
 // give the same bits.  An element from 2^64 on, whose square float32 does not
 // hold, counts as infinite: such a step is left out by its clipping factor.
 namespace {
 
-constexpr int NORM_CHUNK = 8192;
+constexpr int NORM_THREADS = 512, NORM_HOLD = 4;
+constexpr int NORM_CHUNK = 16 * NORM_HOLD * NORM_THREADS;   // bytes
 constexpr float NORM_MOST = 0x1p64f;
+
+template <typename G>
+__device__ __forceinline__ void unpack(const uint4& w, float (&x)[16 / sizeof(G)]) {
+  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(G) == 4) {
+      x[k] = __uint_as_float(a[k]);
+    } else {
+      x[2 * k] = __uint_as_float(a[k] << 16);
+      x[2 * k + 1] = __uint_as_float(a[k] & 0xffff0000u);
+    }
+  }
+}
 
 __device__ __forceinline__ double square(float x) {
   return fabsf(x) < NORM_MOST ? static_cast<double>(x) * x : static_cast<double>(x * x);
 }
 
+// A chunk: consecutive elements of one tensor, of which a thread holds four
+// accesses of 16 bytes (a warp's are next to one another).  201 M elements take
+// 84 us in bf16 and 145 us in float32, 5.3 and 5.9 TB/s with 5 us of launches;
+// with eight elements to a thread at a time, in accesses whose halves of sectors
+// came twice, 129 and 190 us.  256 threads a CTA, two or eight accesses, or the
+// next chunk's loads before this one's sums: 85 to 98 and 145 to 168 us.
+struct Chunk {
+  const char* at;
+  int bytes, wide;      // `wide` of them come in such accesses
+  bool bf16;
+  uint4 w[NORM_HOLD];
+};
+
+template <int CAP>
+__device__ __forceinline__ void load_chunk(const NormParams<CAP>& p, int chunk, Chunk& c) {
+  const int k = find(p.first, p.n, chunk);
+  const NormTensor& t = p.t[k];
+  const int64_t begin = static_cast<int64_t>(chunk - p.first[k]) * NORM_CHUNK;
+  c.at = static_cast<const char*>(t.grad) + begin;
+  c.bf16 = t.bf16;
+  c.bytes = static_cast<int>(min(t.n * (t.bf16 ? 2 : 4) - begin, static_cast<int64_t>(NORM_CHUNK)));
+  c.wide = t.wide ? c.bytes / 16 * 16 : 0;
+#pragma unroll
+  for (int h = 0; h < NORM_HOLD; ++h) {
+    const int i = 16 * (h * NORM_THREADS + threadIdx.x);
+    c.w[h] = i < c.wide ? __ldcg(reinterpret_cast<const uint4*>(c.at + i)) : make_uint4(0, 0, 0, 0);
+  }
+}
+
 template <typename G>
-__device__ double chunk_squares(const NormTensor& t, int64_t begin) {
-  const G* g = static_cast<const G*>(t.grad);
-  const int64_t end = min(begin + NORM_CHUNK, t.n);
-  const int64_t wide = t.wide ? begin + (end - begin) / 8 * 8 : begin;
+__device__ __forceinline__ double squares(const Chunk& c) {
+  constexpr int PER = 16 / sizeof(G);
+  float s[NORM_HOLD];
   double sum = 0.0;
-#pragma unroll 2
-  for (int64_t i = begin + 8 * threadIdx.x; i < wide; i += 8 * blockDim.x) {
-    float x[8];
-    load4(g + i, x);
-    load4(g + i + 4, x + 4);
-    float s = 0.0f;
+  bool plain = true;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s = fmaf(x[k], x[k], s);
-    if (s >= 1e-30f && isfinite(s)) {
-      sum += s;
-      continue;
+  for (int h = 0; h < NORM_HOLD; ++h) {
+    float x[PER];
+    unpack<G>(c.w[h], x);
+    s[h] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) s[h] = fmaf(x[k], x[k], s[h]);
+    plain = plain && s[h] >= 1e-30f && isfinite(s[h]);
+  }
+  if (plain) {
+#pragma unroll
+    for (int h = 0; h < NORM_HOLD; ++h) sum += s[h];
+  } else {   // read again: few chunks need it, and registers are short
+#pragma unroll 1
+    for (int i = 16 * threadIdx.x; i < c.wide; i += 16 * NORM_THREADS) {
+      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(c.at + i));
+      if ((v.x | v.y | v.z | v.w) == 0) continue;
+      float x[PER];
+      unpack<G>(v, x);
+#pragma unroll
+      for (int k = 0; k < PER; ++k) sum += square(x[k]);
     }
-    float most = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) most = larger(most, x[k]);
-    if (most == 0.0f) continue;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sum += square(x[k]);
   }
-  for (int64_t i = wide + threadIdx.x; i < end; i += blockDim.x) {
+  const G* g = reinterpret_cast<const G*>(c.at);
+  for (int i = c.wide / static_cast<int>(sizeof(G)) + threadIdx.x; i < c.bytes / static_cast<int>(sizeof(G));
+       i += NORM_THREADS)
     sum += square(load1(g + i));
-  }
   return sum;
 }
 
@@ -474,13 +529,12 @@ __device__ void write_norm(float* out, double squares, float max_norm) {
 }  // namespace
 
 template <int CAP>
-__global__ void __launch_bounds__(512) relkl_grad_norm_kernel(const __grid_constant__ NormParams<CAP> p) {
+__global__ void __launch_bounds__(NORM_THREADS, 3) relkl_grad_norm_kernel(const __grid_constant__ NormParams<CAP> p) {
   double sum = 0.0;
   for (int chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
-    const int k = find(p.first, p.n, chunk);
-    const int64_t begin = static_cast<int64_t>(chunk - p.first[k]) * NORM_CHUNK;
-    sum += p.t[k].bf16 ? chunk_squares<__nv_bfloat16>(p.t[k], begin)
-                       : chunk_squares<float>(p.t[k], begin);
+    Chunk c;
+    load_chunk(p, chunk, c);
+    sum += c.bf16 ? squares<__nv_bfloat16>(c) : squares<float>(c);
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) {
@@ -491,7 +545,7 @@ __global__ void __launch_bounds__(512) relkl_grad_norm_kernel(const __grid_const
   }
 }
 
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(NORM_THREADS)
 relkl_norm_finish_kernel(const double* partial, int n, float max_norm, float* out) {
   double sum = 0.0;
   for (int i = threadIdx.x; i < n; i += blockDim.x) sum += partial[i];
@@ -500,6 +554,8 @@ relkl_norm_finish_kernel(const double* partial, int n, float max_norm, float* ou
 }
 
 // ------------------------------------------------------------- launches
+int64_t norm_chunks(int64_t n, bool bf16) { return (n * (bf16 ? 2 : 4) + NORM_CHUNK - 1) / NORM_CHUNK; }
+
 namespace {
 
 template <int CAP>
@@ -536,9 +592,9 @@ cudaError_t norm_group(const NormTensor* t, int n, int64_t chunks, int grid, dou
   for (int k = 0; k < n; ++k) {
     p.t[k] = t[k];
     p.first[k] = static_cast<int>(at);
-    at += (t[k].n + NORM_CHUNK - 1) / NORM_CHUNK;
+    at += norm_chunks(t[k].n, t[k].bf16);
   }
-  relkl_grad_norm_kernel<CAP><<<grid, 512, 0, stream>>>(p);
+  relkl_grad_norm_kernel<CAP><<<grid, NORM_THREADS, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -552,8 +608,6 @@ cudaError_t launch_adamw(const AdamwTensor* t, int n, const AdamwPlan& plan, boo
   return adamw_group<kAdamwMost>(t, n, plan, bits8, stream);
 }
 
-int64_t norm_chunks(int64_t n) { return (n + NORM_CHUNK - 1) / NORM_CHUNK; }
-
 // One group's sum: into `out` as a norm where one CTA does all (grid 1), else
 // `grid` partial sums.
 cudaError_t launch_grad_norm(const NormTensor* t, int n, int64_t chunks, int grid, double* partial,
@@ -565,7 +619,7 @@ cudaError_t launch_grad_norm(const NormTensor* t, int n, int64_t chunks, int gri
 
 cudaError_t launch_norm_finish(const double* partial, int n, float max_norm, float* out,
                                cudaStream_t stream) {
-  relkl_norm_finish_kernel<<<1, 512, 0, stream>>>(partial, n, max_norm, out);
+  relkl_norm_finish_kernel<<<1, NORM_THREADS, 0, stream>>>(partial, n, max_norm, out);
   return cudaGetLastError();
 }
 

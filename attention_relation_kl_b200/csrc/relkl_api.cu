@@ -37,7 +37,7 @@ cudaError_t launch_rotary(RotaryParams& p, bool x_bf16, bool y_bf16, bool interl
                           int num_sms, cudaStream_t stream);
 cudaError_t launch_adamw(const AdamwTensor* t, int n, const AdamwPlan& plan, bool bits8,
                          cudaStream_t stream);
-int64_t norm_chunks(int64_t n);
+int64_t norm_chunks(int64_t n, bool bf16);
 cudaError_t launch_grad_norm(const NormTensor* t, int n, int64_t chunks, int grid, double* partial,
                              float* out, float max_norm, cudaStream_t stream);
 cudaError_t launch_norm_finish(const double* partial, int n, float max_norm, float* out,
@@ -958,7 +958,7 @@ relkl_status relkl_grad_norm(int32_t n_tensors, const relkl_norm_tensor* tensors
     if (t.n == 0) continue;
     if (!t.grad || !aligned(t.grad, t.dtype == RELKL_BF16 ? 2 : 4)) return RELKL_ERR_INVALID;
     ++used;
-    all += norm_chunks(t.n);
+    all += norm_chunks(t.n, t.dtype == RELKL_BF16);
     if (all > 0x7fffffffLL) return RELKL_ERR_UNSUPPORTED;
   }
   relkl_status s;
@@ -966,7 +966,7 @@ relkl_status relkl_grad_norm(int32_t n_tensors, const relkl_norm_tensor* tensors
   if ((s = device_info(&dev)) != RELKL_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   double* partial = static_cast<double*>(scratch);
-  const int most = dev.sms * 4 < kNormGrid ? dev.sms * 4 : kNormGrid;
+  const int most = dev.sms * 3 < kNormGrid ? dev.sms * 3 : kNormGrid;
   cudaError_t e = cudaSuccess;
   int sums = 0;
   for (int32_t k = 0; k < n_tensors;) {
@@ -980,8 +980,8 @@ relkl_status relkl_grad_norm(int32_t n_tensors, const relkl_norm_tensor* tensors
       g.grad = t.grad;
       g.n = t.n;
       g.bf16 = t.dtype == RELKL_BF16;
-      g.wide = aligned(t.grad, g.bf16 ? 8 : 16);
-      chunks += norm_chunks(t.n);
+      g.wide = aligned(t.grad, 16);
+      chunks += norm_chunks(t.n, g.bf16);
     }
     if (n == 0) break;
     // a few chunks are summed and finished by one CTA in one launch

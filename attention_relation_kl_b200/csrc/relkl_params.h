@@ -142,8 +142,9 @@ struct AdamwParams {
 };
 
 constexpr int kNormGrid = 1024;     // partial sums of one launch, at most
-// Chunks of 8192 that one CTA sums and finishes alone: with 1, 2 and 4 of them
-// 2.5, 3.3 and 5.2 us, where sums and a second launch take 3.5, 3.9 and 3.9 us.
+// Chunks of 32 KB that one CTA sums and finishes alone: one takes 6.1 us and two
+// 7.5 (bf16) and 8.2 us (float32), a replayed graph's start and end included,
+// where sums and a second launch take 8.2 us.
 constexpr int kNormOneCta = 2;
 
 struct NormTensor {

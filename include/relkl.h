@@ -447,7 +447,7 @@ typedef struct {
 
 /* out[0] = sqrt(sum of grad^2 over all tensors), out[1] = min(1, max_norm /
  * (out[0] + 1e-6)), or NaN where out[0] is not finite (max_norm > 0, infinity
- * allowed; DEVICE float [2], 4-byte aligned).  Squares are summed by eights in
+ * allowed; DEVICE float [2], 4-byte aligned).  The squares of 16 bytes are summed in
  * float32 and beyond in double precision, in an order that the sizes and the
  * GPU fix: the same gradients give the same bits.  A gradient above 1.8e19
  * makes the norm infinite.
