@@ -19,12 +19,11 @@
 // statistics of an 8-bit block stay in the registers of its warp.
 //
 // Measured (B200, copy bandwidth 6.56 TB/s), 201 M float32 weights with bf16
-// copies and gradients: float32 states 823 us, 6.8 TB/s; 8-bit states 549 us, 5.9
-// TB/s (569 us where a lane's eight elements were neighbours, so that each access
-// touched half of its sectors); bf16 weights without copies 498 us.  The 8-bit step is close to the issue rate too:
-// with correctly rounded roots and quotients (99 instructions an element) it took
-// 693 us, with two or more blocks for a warp 250 us more (the second block's loads
-// wait for the first's stores).
+// copies and gradients: float32 states 823 us, 6.8 TB/s; 8-bit states 500 us, 6.5
+// TB/s.  The 8-bit step is close to the issue rate too: with correctly rounded
+// roots and quotients (99 instructions an element) it took 693 us in an earlier
+// form, with one block for a warp 536 us, and with a lane's eight elements next to
+// one another, so that each access touched half of its sectors, 569 us.
 #include <cmath>
 #include <cstdint>
 
@@ -39,7 +38,8 @@ namespace relkl {
 namespace {
 
 constexpr int THREADS = 128;
-constexpr int CHUNK = 1024;             // elements of one CTA: a block of 256 for each warp
+// elements of one CTA: with 8-bit states a block for each warp, or two
+constexpr int CHUNK = 1024;
 constexpr int BLOCK8 = 256;
 constexpr float E4M3_MAX = 448.0f;
 constexpr float E4M3_MIN = 0.001953125f;   // 2^-9, the smallest positive code
@@ -253,11 +253,55 @@ __device__ __forceinline__ float moved_fast(const Hyper& h, float p, float m, fl
   return fmaf(p, h.decay, -h.step * (m * inv));
 }
 
-// One warp, one block of 256: lane l holds elements 4l .. 4l + 3 of each half
-// in wide accesses, so that each covers whole sectors, or l, l + 32, ... (the
-// last block, and tensors that are not aligned for wide ones).
+// Four elements as they come from memory.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+  float4 w;
+  __device__ __forceinline__ void load(const float* p) { w = __ldcg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+  }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  uint2 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = __ldcg(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xffff0000u);
+    v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xffff0000u);
+  }
+};
+
+// What a lane reads of a block: elements 4l .. 4l + 3 of each half, so that an
+// access of the warp covers whole sectors.
+template <typename G, typename P>
+struct Block8 {
+  Four<G> g[2];
+  Four<P> p[2];
+  uint32_t m[2], r[2];
+  float ms, rs;
+  __device__ __forceinline__ void load(const AdamwTensor& t, int64_t blk) {
+    const int64_t at = blk * BLOCK8 + 4 * (threadIdx.x & 31);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      m[k] = __ldcg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + at + 128 * k));
+      r[k] = __ldcg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + at + 128 * k));
+      g[k].load(static_cast<const G*>(t.grad) + at + 128 * k);
+      p[k].load(static_cast<const P*>(t.param) + at + 128 * k);
+    }
+    ms = __ldcg(t.m_scale + blk);
+    rs = __ldcg(t.v_scale + blk);
+  }
+};
+
+// One warp, one block of 256, held as above (WIDE) or element by element,
+// l, l + 32, ... to a lane (the last block, and tensors that are not aligned
+// for wide accesses).
 template <typename G, typename P, bool WIDE>
-__device__ __forceinline__ void block8(const AdamwTensor& t, const Hyper& h, int64_t blk) {
+__device__ __forceinline__ void block8(const AdamwTensor& t, const Hyper& h, int64_t blk,
+                                       const Block8<G, P>* held = nullptr) {
   const int lane = threadIdx.x & 31;
   const int64_t first = blk * BLOCK8;
   const G* g = static_cast<const G*>(t.grad) + first;
@@ -267,22 +311,20 @@ __device__ __forceinline__ void block8(const AdamwTensor& t, const Hyper& h, int
   const int left = static_cast<int>(min(t.n - first, static_cast<int64_t>(BLOCK8)));
   float gg[8], pp[8], mm[8], rr[8], vv[8];
   const int at = 4 * lane;
-  const float ms = __ldcg(t.m_scale + blk), rs = __ldcg(t.v_scale + blk);
+  float ms, rs;
   if constexpr (WIDE) {
-    uint32_t mq[2], rq[2];
+    ms = held->ms;
+    rs = held->rs;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      mq[k] = __ldcg(reinterpret_cast<const uint32_t*>(mc + at + 128 * k));
-      rq[k] = __ldcg(reinterpret_cast<const uint32_t*>(rc + at + 128 * k));
-      load4(g + at + 128 * k, gg + 4 * k);
-      load4(p + at + 128 * k, pp + 4 * k);
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      decode4(mq[k], mm + 4 * k);
-      decode4(rq[k], rr + 4 * k);
+      held->g[k].get(gg + 4 * k);
+      held->p[k].get(pp + 4 * k);
+      decode4(held->m[k], mm + 4 * k);
+      decode4(held->r[k], rr + 4 * k);
     }
   } else {
+    ms = __ldcg(t.m_scale + blk);
+    rs = __ldcg(t.v_scale + blk);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int i = lane + 32 * k;
@@ -361,15 +403,27 @@ __device__ __forceinline__ void block8(const AdamwTensor& t, const Hyper& h, int
   }
 }
 
-template <typename G, typename P>
+template <typename G, typename P, int PER_WARP>
 __device__ void chunk8(const AdamwTensor& t, const Hyper& h, int64_t begin) {
-  const int64_t last = (min(begin + CHUNK, t.n) + BLOCK8 - 1) / BLOCK8;
+  const int64_t last = (min(begin + PER_WARP * CHUNK, t.n) + BLOCK8 - 1) / BLOCK8;
+  const int64_t b = begin / BLOCK8 + (threadIdx.x >> 5) * PER_WARP;
+  if (t.wide && (b + PER_WARP) * BLOCK8 <= t.n) {
+    Block8<G, P> held[PER_WARP];
+#pragma unroll
+    for (int k = 0; k < PER_WARP; ++k) held[k].load(t, b + k);
+#pragma unroll
+    for (int k = 0; k < PER_WARP; ++k) block8<G, P, true>(t, h, b + k, &held[k]);
+    return;
+  }
 #pragma unroll 1
-  for (int64_t b = begin / BLOCK8 + (threadIdx.x >> 5); b < last; b += THREADS / 32) {
-    if (t.wide && (b + 1) * BLOCK8 <= t.n)
-      block8<G, P, true>(t, h, b);
-    else
-      block8<G, P, false>(t, h, b);
+  for (int k = 0; k < PER_WARP && b + k < last; ++k) {
+    if (t.wide && (b + k + 1) * BLOCK8 <= t.n) {
+      Block8<G, P> held;
+      held.load(t, b + k);
+      block8<G, P, true>(t, h, b + k, &held);
+    } else {
+      block8<G, P, false>(t, h, b + k);
+    }
   }
 }
 
@@ -386,18 +440,19 @@ __device__ __forceinline__ int find(const int (&first)[CAP], int n, int block) {
 
 }  // namespace
 
-template <int CAP, bool BITS8>
-__global__ void __launch_bounds__(THREADS, 8) relkl_adamw_kernel(const __grid_constant__ AdamwParams<CAP> p) {
+// BLOCKS: 8-bit blocks of one warp, 0 with float32 states
+template <int CAP, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS == 2 ? 7 : 8) relkl_adamw_kernel(const __grid_constant__ AdamwParams<CAP> p) {
   const int k = find(p.first, p.n, blockIdx.x);
   const AdamwTensor& t = p.t[k];
   const Hyper h = hyper(p.plan, t);
   if (h.skip) return;
-  const int64_t begin = static_cast<int64_t>(blockIdx.x - p.first[k]) * CHUNK;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - p.first[k]) * (BLOCKS == 2 ? 2 * CHUNK : CHUNK);
   using H = __nv_bfloat16;
 #define RELKL_CHUNK(G, P)                \
   do {                                   \
-    if constexpr (BITS8)                 \
-      chunk8<G, P>(t, h, begin);         \
+    if constexpr (BLOCKS > 0)            \
+      chunk8<G, P, BLOCKS>(t, h, begin); \
     else                                 \
       chunk32<G, P>(t, h, begin);        \
   } while (0)
@@ -558,25 +613,36 @@ int64_t norm_chunks(int64_t n, bool bf16) { return (n * (bf16 ? 2 : 4) + NORM_CH
 
 namespace {
 
-template <int CAP>
-cudaError_t adamw_group(const AdamwTensor* t, int n, const AdamwPlan& plan, bool bits8,
-                        cudaStream_t stream) {
+template <int CAP, int BLOCKS>
+cudaError_t adamw_group(const AdamwTensor* t, int n, const AdamwPlan& plan, cudaStream_t stream) {
   AdamwParams<CAP> p;
   p.plan = plan;
   p.n = n;
   int64_t blocks = 0;
-  const int chunk = CHUNK;
+  constexpr int chunk = BLOCKS == 2 ? 2 * CHUNK : CHUNK;
   for (int k = 0; k < n; ++k) {
     p.t[k] = t[k];
     p.first[k] = static_cast<int>(blocks);
     blocks += (t[k].n + chunk - 1) / chunk;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   }
-  if (bits8)
-    relkl_adamw_kernel<CAP, true><<<static_cast<unsigned>(blocks), THREADS, 0, stream>>>(p);
-  else
-    relkl_adamw_kernel<CAP, false><<<static_cast<unsigned>(blocks), THREADS, 0, stream>>>(p);
+  relkl_adamw_kernel<CAP, BLOCKS><<<static_cast<unsigned>(blocks), THREADS, 0, stream>>>(p);
   return cudaGetLastError();
+}
+
+// Elements from which a warp takes two 8-bit blocks.  It loads both before it
+// works on the first, and looks up tensor and scalars once: 201 M elements take
+// 500 us instead of 536 (float32 weights, bf16 gradients and copies), 406
+// instead of 465 (all bf16), 485 instead of 521 (all float32).  Fewer fill the
+// SMs worse that way: 34 M 96, 74, 94 and 94, 82, 96 us, 12.6 M 47, 33, 47 and 41,
+// 37, 45, 3.1 M 25, 14, 25 and 16, 14, 18.
+constexpr int64_t kAdamwTwoBlocks = int64_t(1) << 25;
+
+template <int BLOCKS>
+cudaError_t adamw_blocks(const AdamwTensor* t, int n, const AdamwPlan& plan, cudaStream_t stream) {
+  if (n <= kAdamwFew) return adamw_group<kAdamwFew, BLOCKS>(t, n, plan, stream);
+  if (n <= kAdamwSome) return adamw_group<kAdamwSome, BLOCKS>(t, n, plan, stream);
+  return adamw_group<kAdamwMost, BLOCKS>(t, n, plan, stream);
 }
 
 template <int CAP>
@@ -603,9 +669,10 @@ cudaError_t norm_group(const NormTensor* t, int n, int64_t chunks, int grid, dou
 // Tensors are those with elements, at most kAdamwMost of them.
 cudaError_t launch_adamw(const AdamwTensor* t, int n, const AdamwPlan& plan, bool bits8,
                          cudaStream_t stream) {
-  if (n <= kAdamwFew) return adamw_group<kAdamwFew>(t, n, plan, bits8, stream);
-  if (n <= kAdamwSome) return adamw_group<kAdamwSome>(t, n, plan, bits8, stream);
-  return adamw_group<kAdamwMost>(t, n, plan, bits8, stream);
+  if (!bits8) return adamw_blocks<0>(t, n, plan, stream);
+  int64_t all = 0;
+  for (int k = 0; k < n; ++k) all += t[k].n;
+  return all >= kAdamwTwoBlocks ? adamw_blocks<2>(t, n, plan, stream) : adamw_blocks<1>(t, n, plan, stream);
 }
 
 // One group's sum: into `out` as a norm where one CTA does all (grid 1), else

@@ -446,3 +446,37 @@ def test_norm_whose_squares_leave_float32(sizes, dtype):
             grads[0][at] = 2.0 ** 63
         got, want = rk.relkl_grad_norm(grads), math.sqrt(sum(float((_f64(g) ** 2).sum()) for g in grads))
         assert abs(float(got[0]) - want) <= 6 * U * want
+
+
+# many elements: a warp holds two blocks of 256, and pieces of the same tensors one at a time
+# give the same bits
+@pytest.mark.parametrize("pt,gt,copies", [(F32, BF16, True), (BF16, BF16, False), (F32, F32, False),
+                                          (BF16, F32, True)])
+def test_many_elements_and_their_pieces(pt, gt, copies):
+    sizes = [(1 << 25) - 256, 256 * 7, 3, 512 * 9 + 1, 256, 70000, 511]
+    params, grads, states, cs = _make([2 ** 20 + 256 * 3], 8, pt, gt, 13, copies=copies)
+    tile = lambda x, n: x.repeat(-(-n // x.numel()))[:n].clone()  # noqa: E731
+    first = [params[0], grads[0], *states[0][:2]]
+    whole = []
+    for k, n in enumerate(sizes):
+        raw = [tile(x.view(torch.uint8) if x.dtype == E4M3 else x, n + 1)[int(k == 5):][:n] for x in first]
+        blocks = -(-n // 256)
+        whole.append([raw[0], raw[1], rk.AdamWState(raw[2].view(E4M3), raw[3].view(E4M3),
+                                                   tile(states[0][2], blocks), tile(states[0][3], blocks)),
+                      torch.zeros(n, dtype=BF16, device="cuda")])
+    twin = [[p.clone(), g, rk.AdamWState(*(x.clone() for x in s)), c.clone()] for p, g, s, c in whole]
+
+    def step(rows):
+        rk.relkl_adamw([r[0] for r in rows], [r[1] for r in rows], [r[2] for r in rows], step=4,
+                       weight_decay=0.1, copies=[r[3] for r in rows] if copies else None, **HYPER)
+
+    step(whole)
+    for p, g, s, c in twin:
+        for a in range(0, p.numel(), 1 << 23):
+            b = min(a + (1 << 23), p.numel())
+            step([[p[a:b], g[a:b], rk.AdamWState(s.m[a:b], s.v[a:b], s.m_scale[a // 256:-(-b // 256)],
+                                                 s.v_scale[a // 256:-(-b // 256)]), c[a:b]]])
+    for x, y in zip(whole, twin):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[3], y[3])
+        for a, b in zip(x[2], y[2]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
