@@ -128,3 +128,16 @@ def test_given_frequencies_equal_the_base():
     for r in "qkv":
         # both round the same gradient to bf16 (2^-8), its float32 sums add in another order
         assert float((a[r] - b[r]).abs().max()) <= 2.0 ** -7 * float(a[r].abs().max())
+
+
+# the tokens are coded once for all relations, or by each one's product: the same bits
+@pytest.mark.parametrize("B,N", [(2, 0), (1, 1), (4, 1), (5, 1), (2, 150)])
+def test_teacher_relations_equal_one_after_the_other(B, N):
+    gen, freqs = torch.Generator().manual_seed(3), rk.rotary_freqs(64)
+    h = torch.randn(B, N, 136, generator=gen).to(BF16).cuda()
+    weights = {r: rk.relkl_quantize_rows(torch.randn(n * 64, 136, generator=gen).cuda())
+               for r, n in dict(q=3, k=1, v=1).items()}
+    got = rk.teacher_relations_i8(h, weights, 64, freqs)
+    for r in weights:
+        (one,) = rk.teacher_relations_i8(h, {r: weights[r]}, 64, freqs).values()
+        assert torch.equal(got[r], one)
