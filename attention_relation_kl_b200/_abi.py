@@ -179,6 +179,10 @@ def marshal():
         except ImportError as e:
             raise ImportError("the marshalling module is missing or was built for another torch; build it "
                               f"with `python -m attention_relation_kl_b200.build` ({e})") from e
+        library = lib()
+        _marshal.bind(*(ctypes.cast(getattr(library, name), ctypes.c_void_p).value
+                        for name in ("relkl_rotary", "relkl_linear_i8", "relkl_linear_i8_bytes",
+                                     "relkl_grad_norm", "relkl_grad_norm_bytes")))
         _MARSHAL = _marshal
     return _MARSHAL
 

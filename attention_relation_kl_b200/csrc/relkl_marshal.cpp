@@ -1,8 +1,9 @@
-// Marshalling of tensor lists into the C ABI's records, for the calls whose
-// time on the host is the marshalling: a step over many small tensors, a
-// rotation of a single token.  Checks and packing only: nothing here allocates
-// device memory, launches or computes.  What took 2.4 us a tensor in Python
-// takes 0.1 us.
+// Marshalling of tensors into the C ABI's records, for the calls whose time on
+// the host is the marshalling: a step over many small tensors, a rotation or a
+// product of a single token.  Checks, packing, and where a call has outputs or
+// scratch of its own also those and the call.  What took 2.4 us a tensor in
+// Python takes 0.1 us; a product of one row, 11.7 us in all, takes 6.4, of 77
+// rows 9.2 instead of 16.4, and a rotation with two outputs 7.5 instead of 13.2.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -10,6 +11,8 @@
 #include <vector>
 
 #include <c10/core/impl/VirtualGuardImpl.h>
+#include <ATen/Functions.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/autograd/variable.h>
@@ -69,6 +72,12 @@ PyObject* guarded(F&& f) {
   try {
     return f();
   } catch (const Raised&) {
+  } catch (const c10::OutOfMemoryError& e) {
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, e.what_without_backtrace());
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {
@@ -81,6 +90,48 @@ template <typename T>
 PyObject* bytes_of(const std::vector<T>& v) {
   return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(v.data()),
                                    static_cast<Py_ssize_t>(v.size() * sizeof(T)));
+}
+
+// The library's entry points (bind).
+struct Library {
+  decltype(&relkl_rotary) rotary;
+  decltype(&relkl_linear_i8) linear_i8;
+  decltype(&relkl_linear_i8_bytes) linear_i8_bytes;
+  decltype(&relkl_grad_norm) grad_norm;
+  decltype(&relkl_grad_norm_bytes) grad_norm_bytes;
+} library = {};
+
+// bind(relkl_rotary, relkl_linear_i8, relkl_linear_i8_bytes, relkl_grad_norm,
+//      relkl_grad_norm_bytes): their addresses
+PyObject* bind(PyObject*, PyObject* args) {
+  return guarded([&]() -> PyObject* {
+    unsigned long long a, b, c, d, e;
+    if (!PyArg_ParseTuple(args, "KKKKK", &a, &b, &c, &d, &e)) throw Raised{};
+    library.rotary = reinterpret_cast<decltype(library.rotary)>(static_cast<uintptr_t>(a));
+    library.linear_i8 = reinterpret_cast<decltype(library.linear_i8)>(static_cast<uintptr_t>(b));
+    library.linear_i8_bytes = reinterpret_cast<decltype(library.linear_i8_bytes)>(static_cast<uintptr_t>(c));
+    library.grad_norm = reinterpret_cast<decltype(library.grad_norm)>(static_cast<uintptr_t>(d));
+    library.grad_norm_bytes = reinterpret_cast<decltype(library.grad_norm_bytes)>(static_cast<uintptr_t>(e));
+    Py_RETURN_NONE;
+  });
+}
+
+// Other threads run while device memory is had or a launch waits for its turn.
+struct Released {
+  PyThreadState* state;
+  Released() : state(PyEval_SaveThread()) {}
+  ~Released() { PyEval_RestoreThread(state); }
+  Released(const Released&) = delete;
+  Released& operator=(const Released&) = delete;
+};
+
+at::ScalarType output_type(PyObject* o) {
+  if (THPDtype_Check(o)) {
+    const at::ScalarType t = reinterpret_cast<THPDtype*>(o)->scalar_type;
+    if (t == at::kBFloat16 || t == at::kFloat) return t;
+  }
+  PyErr_Format(PyExc_TypeError, "unsupported output dtype %R", o);
+  throw Raised{};
 }
 
 double number(PyObject* o) {
@@ -236,6 +287,35 @@ PyObject* norm(PyObject*, PyObject* arg) {
   });
 }
 
+// grad_norm(a gradient, records of norm, max_norm, out, stream) -> (status, out); out None: a
+// tensor on the gradient's device
+PyObject* grad_norm(PyObject*, PyObject* args) {
+  return guarded([&]() -> PyObject* {
+    PyObject *go, *yo;
+    const char* records;
+    Py_ssize_t bytes;
+    double max_norm;
+    unsigned long long stream;
+    if (!PyArg_ParseTuple(args, "Oy#dOK", &go, &records, &bytes, &max_norm, &yo, &stream)) throw Raised{};
+    if (!library.grad_norm) raise(PyExc_RuntimeError, "no library");
+    const at::Tensor& g = tensor(go, "gradients");
+    at::Tensor out;
+    if (yo != Py_None) out = tensor(yo, "out");
+    const int32_t n = static_cast<int32_t>(bytes / static_cast<Py_ssize_t>(sizeof(relkl_norm_tensor)));
+    relkl_status status;
+    {
+      const Released released;
+      if (yo == Py_None) out = at::empty({2}, g.options().dtype(at::kFloat));
+      const size_t need = library.grad_norm_bytes(n);
+      const at::Tensor scratch = at::empty({static_cast<int64_t>(need)}, g.options().dtype(at::kByte));
+      status = library.grad_norm(n, reinterpret_cast<const relkl_norm_tensor*>(records),
+                                 static_cast<float>(max_norm), static_cast<float*>(out.data_ptr()),
+                                 scratch.data_ptr(), need, reinterpret_cast<void*>(stream));
+    }
+    return Py_BuildValue("(iN)", static_cast<int>(status), THPVariable_Wrap(out));
+  });
+}
+
 // A [B, H, N, d] tensor's rows are contiguous (a dimension of one element has any stride).
 bool rows_contiguous(const at::Tensor& t) { return t.size(3) <= 1 || t.stride(3) == 1; }
 
@@ -270,23 +350,37 @@ PyObject* rotary_inputs(PyObject*, PyObject* args) {
   });
 }
 
-// rotary(xs, outs, apply, inv_freq, positions, interleaved, inverse, mscale, pos_scale,
-//        pos_offset) -> (relkl_rotary_tensor records, relkl_rotary_plan), of inputs that
-// rotary_inputs has accepted
+// rotary(xs, outs, output type, apply, inv_freq, positions, interleaved, inverse, mscale,
+//        pos_scale, pos_offset, stream) -> (status, outputs), of inputs that rotary_inputs has
+// accepted; outs None: contiguous tensors of the output type
 PyObject* rotary(PyObject*, PyObject* args) {
   return guarded([&]() -> PyObject* {
-    PyObject *xo, *yo, *ao, *fo, *po;
+    PyObject *xo, *yo, *to, *ao, *fo, *po;
     int interleaved, inverse;
     double mscale, pos_scale, pos_offset;
-    if (!PyArg_ParseTuple(args, "OOOOOppddd", &xo, &yo, &ao, &fo, &po, &interleaved, &inverse, &mscale,
-                          &pos_scale, &pos_offset))
+    unsigned long long stream;
+    if (!PyArg_ParseTuple(args, "OOOOOOppdddK", &xo, &yo, &to, &ao, &fo, &po, &interleaved, &inverse,
+                          &mscale, &pos_scale, &pos_offset, &stream))
       throw Raised{};
-    const Items xs(xo, "expected a sequence of tensors"), ys(yo, "out must be a sequence of tensors");
+    if (!library.rotary) raise(PyExc_RuntimeError, "no library");
+    const Items xs(xo, "expected a sequence of tensors");
     const Py_ssize_t n = xs.size();
-    if (ys.size() != n) raise(PyExc_ValueError, "apply and out need one entry for each tensor");
+    // held by references of their own: another thread may change the lists meanwhile
+    std::vector<at::Tensor> inputs, outputs;
+    for (Py_ssize_t k = 0; k < n; ++k) inputs.push_back(tensor(xs[k], "xs"));
+    if (yo == Py_None) {
+      const at::ScalarType type = output_type(to);
+      const Released released;
+      for (const at::Tensor& x : inputs) outputs.push_back(at::empty(x.sizes(), x.options().dtype(type)));
+    } else {
+      const Items ys(yo, "out must be a sequence of tensors");
+      for (Py_ssize_t k = 0; k < ys.size(); ++k) outputs.push_back(tensor(ys[k], "out"));
+    }
+    if (n == 0 || static_cast<Py_ssize_t>(outputs.size()) != n)
+      raise(PyExc_ValueError, "apply and out need one entry for each tensor");
     const Items apply(ao == Py_None ? xo : ao, "apply must be a sequence");
     if (apply.size() != n) raise(PyExc_ValueError, "apply and out need one entry for each tensor");
-    const at::Tensor &x0 = tensor(xs[0], "xs"), &y0 = tensor(ys[0], "out"), &f = tensor(fo, "inv_freq");
+    const at::Tensor &x0 = inputs[0], &y0 = outputs[0], &f = tensor(fo, "inv_freq");
     const int index = static_cast<int>(x0.get_device());
     relkl_rotary_plan plan = {};
     plan.B = static_cast<int32_t>(x0.size(0));
@@ -317,7 +411,7 @@ PyObject* rotary(PyObject*, PyObject* args) {
     }
     std::vector<relkl_rotary_tensor> out(static_cast<size_t>(n));
     for (Py_ssize_t k = 0; k < n; ++k) {
-      const at::Tensor &x = tensor(xs[k], "xs"), &y = tensor(ys[k], "out");
+      const at::Tensor &x = inputs[k], &y = outputs[k];
       if (y.sizes() != x.sizes() || y.scalar_type() != y0.scalar_type() || !y.is_cuda() ||
           y.get_device() != index || !rows_contiguous(y))
         raise(PyExc_ValueError,
@@ -335,8 +429,15 @@ PyObject* rotary(PyObject*, PyObject* args) {
       if (turns < 0) throw Raised{};
       t.apply = turns;
     }
-    return Py_BuildValue("(Ny#)", bytes_of(out), reinterpret_cast<const char*>(&plan),
-                         static_cast<Py_ssize_t>(sizeof(plan)));
+    relkl_status status;
+    {
+      const Released released;
+      status = library.rotary(static_cast<int32_t>(n), out.data(), &plan, reinterpret_cast<void*>(stream));
+    }
+    PyObject* list = PyList_New(n);
+    if (!list) throw Raised{};
+    for (Py_ssize_t k = 0; k < n; ++k) PyList_SET_ITEM(list, k, THPVariable_Wrap(outputs[k]));
+    return Py_BuildValue("(iN)", static_cast<int>(status), list);
   });
 }
 
@@ -345,63 +446,90 @@ PyObject* rotary(PyObject*, PyObject* args) {
   throw Raised{};
 }
 
-// matrix(x, what) -> (rows, K, row stride, address, relkl_dtype, device index) of x [..., K],
-// whose rows must follow one another evenly
+struct Matrix {
+  int64_t rows, K, stride;
+  uintptr_t at;
+  int32_t type;
+};
+
+// The rows of x [..., K], which must follow one another evenly.
+Matrix matrix_of(const at::Tensor& x, const char* what) {
+  if (!x.is_cuda()) raise_about(PyExc_ValueError, what, "must be a CUDA tensor (there is no CPU path)");
+  const int32_t type = element(x, what);
+  const int64_t dims = x.dim();
+  if (dims < 1) raise_about(PyExc_ValueError, what, "must have at least one dimension");
+  const int64_t K = x.size(dims - 1);
+  if (K > 1 && x.stride(dims - 1) != 1)
+    raise_about(PyExc_ValueError, what, "must have a contiguous last dimension");
+  if (K > 0x7fffffff) raise_about(PyExc_ValueError, what, "has rows of more than 2^31 - 1 elements");
+  int64_t rows = 1, stride = K, next = -1;   // next: the stride of a dimension around those seen
+  for (int64_t i = dims - 2; i >= 0; --i) {
+    const int64_t n = x.size(i);
+    rows *= n;
+    if (n <= 1) continue;
+    if (next < 0)
+      stride = x.stride(i);
+    else if (x.stride(i) != next)
+      raise_about(PyExc_ValueError, what, "must have rows that follow one another at one stride");
+    next = x.stride(i) * n;
+  }
+  return Matrix{rows, K, stride, reinterpret_cast<uintptr_t>(x.const_data_ptr()), type};
+}
+
+// An int8 matrix laid out as relkl_quantize_rows lays it out; index -1: on any device.
+Matrix codes_of(const at::Tensor& q, const char* what, int index) {
+  if (!q.is_cuda() || (index >= 0 && q.get_device() != index))
+    raise_about(PyExc_ValueError, what, "must be a CUDA tensor on the inputs' device (there is no CPU path)");
+  if (q.scalar_type() != at::kChar || q.dim() != 2)
+    raise_about(PyExc_ValueError, what, "must be an int8 matrix");
+  const int64_t rows = q.size(0), K = q.size(1);
+  int64_t stride = q.stride(0);
+  if (rows <= 1) stride = (K + 15) / 16 * 16;   // one row has no stride
+  const uintptr_t at = reinterpret_cast<uintptr_t>(q.const_data_ptr());
+  if ((K > 1 && q.stride(1) != 1) || stride % 16 || stride < K || at % 16)
+    raise_about(PyExc_ValueError, what,
+                "must have contiguous rows that start at 16-byte boundaries, as relkl_quantize_rows "
+                "lays them out");
+  return Matrix{rows, K, stride, at, 0};
+}
+
+// A float32 vector of n, or None.
+const float* vector_of(PyObject* o, long long n, const char* what, int index) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& v = tensor(o, what);
+  if (v.scalar_type() != at::kFloat || v.dim() != 1 || v.numel() != n || !v.is_contiguous() || !v.is_cuda() ||
+      v.get_device() != index) {
+    PyErr_Format(PyExc_ValueError, "%s must be a contiguous float32 vector of %lld on the inputs' device",
+                 what, n);
+    throw Raised{};
+  }
+  return static_cast<const float*>(v.const_data_ptr());
+}
+
+// matrix(x, what) -> (rows, K, row stride, address, relkl_dtype, device index)
 PyObject* matrix(PyObject*, PyObject* args) {
   return guarded([&]() -> PyObject* {
     PyObject* o;
     const char* what;
     if (!PyArg_ParseTuple(args, "Os", &o, &what)) throw Raised{};
     const at::Tensor& x = tensor(o, what);
-    if (!x.is_cuda()) raise_about(PyExc_ValueError, what, "must be a CUDA tensor (there is no CPU path)");
-    const int32_t type = element(x, what);
-    const int64_t dims = x.dim();
-    if (dims < 1) raise_about(PyExc_ValueError, what, "must have at least one dimension");
-    const int64_t K = x.size(dims - 1);
-    if (K > 1 && x.stride(dims - 1) != 1)
-      raise_about(PyExc_ValueError, what, "must have a contiguous last dimension");
-    if (K > 0x7fffffff) raise_about(PyExc_ValueError, what, "has rows of more than 2^31 - 1 elements");
-    int64_t rows = 1, stride = K, next = -1;   // next: the stride of a dimension around those seen
-    for (int64_t i = dims - 2; i >= 0; --i) {
-      const int64_t n = x.size(i);
-      rows *= n;
-      if (n <= 1) continue;
-      if (next < 0)
-        stride = x.stride(i);
-      else if (x.stride(i) != next)
-        raise_about(PyExc_ValueError, what, "must have rows that follow one another at one stride");
-      next = x.stride(i) * n;
-    }
-    return Py_BuildValue("(LLLKii)", static_cast<long long>(rows), static_cast<long long>(K),
-                         static_cast<long long>(stride),
-                         static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(x.const_data_ptr())),
-                         static_cast<int>(type), static_cast<int>(x.get_device()));
+    const Matrix m = matrix_of(x, what);
+    return Py_BuildValue("(LLLKii)", static_cast<long long>(m.rows), static_cast<long long>(m.K),
+                         static_cast<long long>(m.stride), static_cast<unsigned long long>(m.at),
+                         static_cast<int>(m.type), static_cast<int>(x.get_device()));
   });
 }
 
-// codes(q, what, device index) -> (rows, K, row stride, address) of an int8 matrix laid out as
-// relkl_quantize_rows lays it out; index -1: any device
+// codes(q, what, device index) -> (rows, K, row stride, address)
 PyObject* codes(PyObject*, PyObject* args) {
   return guarded([&]() -> PyObject* {
     PyObject* o;
     const char* what;
     int index;
     if (!PyArg_ParseTuple(args, "Osi", &o, &what, &index)) throw Raised{};
-    const at::Tensor& q = tensor(o, what);
-    if (!q.is_cuda() || (index >= 0 && q.get_device() != index))
-      raise_about(PyExc_ValueError, what, "must be a CUDA tensor on the inputs' device (there is no CPU path)");
-    if (q.scalar_type() != at::kChar || q.dim() != 2)
-      raise_about(PyExc_ValueError, what, "must be an int8 matrix");
-    const int64_t rows = q.size(0), K = q.size(1);
-    int64_t stride = q.stride(0);
-    if (rows <= 1) stride = (K + 15) / 16 * 16;   // one row has no stride
-    const uintptr_t at = reinterpret_cast<uintptr_t>(q.const_data_ptr());
-    if ((K > 1 && q.stride(1) != 1) || stride % 16 || stride < K || at % 16)
-      raise_about(PyExc_ValueError, what,
-                  "must have contiguous rows that start at 16-byte boundaries, as relkl_quantize_rows "
-                  "lays them out");
-    return Py_BuildValue("(LLLK)", static_cast<long long>(rows), static_cast<long long>(K),
-                         static_cast<long long>(stride), static_cast<unsigned long long>(at));
+    const Matrix m = codes_of(tensor(o, what), what, index);
+    return Py_BuildValue("(LLLK)", static_cast<long long>(m.rows), static_cast<long long>(m.K),
+                         static_cast<long long>(m.stride), static_cast<unsigned long long>(m.at));
   });
 }
 
@@ -413,15 +541,56 @@ PyObject* vector(PyObject*, PyObject* args) {
     long long n;
     int index;
     if (!PyArg_ParseTuple(args, "OLsi", &o, &n, &what, &index)) throw Raised{};
-    if (o == Py_None) return PyLong_FromLong(0);
-    const at::Tensor& v = tensor(o, what);
-    if (v.scalar_type() != at::kFloat || v.dim() != 1 || v.numel() != n || !v.is_contiguous() || !v.is_cuda() ||
-        v.get_device() != index) {
-      PyErr_Format(PyExc_ValueError, "%s must be a contiguous float32 vector of %lld on the inputs' device",
-                   what, n);
+    return PyLong_FromVoidPtr(const_cast<float*>(vector_of(o, n, what, index)));
+  });
+}
+
+// linear_i8(x, w, w_scale, bias, output type, out, ws, stream) -> (status, y); out None: a
+// contiguous tensor, else one of the right shape and type on x's device that meets no input
+PyObject* linear_i8(PyObject*, PyObject* args) {
+  return guarded([&]() -> PyObject* {
+    PyObject *xo, *wo, *so, *bo, *to, *yo, *ro;
+    unsigned long long stream;
+    if (!PyArg_ParseTuple(args, "OOOOOOOK", &xo, &wo, &so, &bo, &to, &yo, &ro, &stream)) throw Raised{};
+    if (!library.linear_i8) raise(PyExc_RuntimeError, "no library");
+    const at::Tensor &xt = tensor(xo, "x"), &wt = tensor(wo, "w"), &record = tensor(ro, "ws");
+    const Matrix x = matrix_of(xt, "x");
+    const int index = static_cast<int>(xt.get_device());
+    const Matrix w = codes_of(wt, "w", index);
+    if (w.K != x.K) {
+      PyErr_Format(PyExc_ValueError, "x has rows of %lld elements, w of %lld", static_cast<long long>(x.K),
+                   static_cast<long long>(w.K));
       throw Raised{};
     }
-    return PyLong_FromVoidPtr(const_cast<void*>(v.const_data_ptr()));
+    if (w.rows > 0x7fffffff) raise(PyExc_ValueError, "w has more than 2^31 - 1 channels");
+    if (so == Py_None) raise(PyExc_ValueError, "w_scale must be a float32 vector");
+    const float* scale = vector_of(so, w.rows, "w_scale", index);
+    const float* bias = vector_of(bo, w.rows, "bias", index);
+    const int32_t K = static_cast<int32_t>(x.K);
+    const at::ScalarType type = output_type(to);
+    at::Tensor out, scratch;
+    if (yo != Py_None) out = tensor(yo, "out");
+    const size_t bytes = library.linear_i8_bytes(x.rows, K);
+    {
+      const Released released;
+      if (yo == Py_None) {
+        c10::SmallVector<int64_t, 5> shape(xt.sizes().begin(), xt.sizes().end());
+        shape.back() = w.rows;
+        out = at::empty(shape, xt.options().dtype(type));
+      }
+      if (bytes) scratch = at::empty({static_cast<int64_t>(bytes)}, xt.options().dtype(at::kByte));
+    }
+    const Matrix y = matrix_of(out, "out");
+    relkl_status status;
+    {
+      const Released released;
+      status = library.linear_i8(x.rows, static_cast<int32_t>(w.rows), K, reinterpret_cast<const void*>(x.at),
+                                 x.type, x.stride, reinterpret_cast<const int8_t*>(w.at), w.stride, scale, bias,
+                                 reinterpret_cast<void*>(y.at), y.type, y.stride,
+                                 bytes ? scratch.data_ptr() : nullptr, bytes, record.data_ptr(),
+                                 static_cast<size_t>(record.numel()), reinterpret_cast<void*>(stream));
+    }
+    return Py_BuildValue("(iN)", static_cast<int>(status), THPVariable_Wrap(out));
   });
 }
 
@@ -430,8 +599,11 @@ PyMethodDef methods[] = {
     {"written", written, METH_O, "marks tensors as changed in place"},
     {"graph_elsewhere", graph_elsewhere, METH_O, "whether a gradient would leave the current stream"},
     {"norm", norm, METH_O, "records of relkl_grad_norm"},
+    {"grad_norm", grad_norm, METH_VARARGS, "relkl_grad_norm"},
     {"rotary_inputs", rotary_inputs, METH_VARARGS, "checks of relkl_rotary's inputs"},
-    {"rotary", rotary, METH_VARARGS, "records of relkl_rotary"},
+    {"bind", bind, METH_VARARGS, "gives the library's entry points"},
+    {"rotary", rotary, METH_VARARGS, "relkl_rotary"},
+    {"linear_i8", linear_i8, METH_VARARGS, "relkl_linear_i8"},
     {"matrix", matrix, METH_VARARGS, "layout of a matrix of rows"},
     {"codes", codes, METH_VARARGS, "layout of a matrix of codes"},
     {"vector", vector, METH_VARARGS, "address of a float32 vector"},

@@ -111,25 +111,16 @@ def relkl_linear_i8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
     Returns [..., cols] of ``out_dtype`` (x's type without it); one kernel for up to 4 rows.
     ``out`` may have rows at any one stride; its addresses may not meet an input's."""
     m = _abi.marshal()
-    rows, K, stride, x_ptr, x_type, index = m.matrix(x, "x")
-    cols, Kw, w_stride, w_ptr = m.codes(w, "w", index)
-    if Kw != K:
-        raise ValueError(f"x has rows of {K} elements, w of {Kw}")
-    s, b = m.vector(w_scale, cols, "w_scale", index), m.vector(bias, cols, "bias", index)
+    index = m.matrix(x, "x")[5]
     device = x.device
     out_dtype = x.dtype if out_dtype is None else out_dtype
-    lib = _abi.lib()
+    if out is not None:
+        cols = m.codes(w, "w", index)[0]
+        _output(out, (*x.shape[:-1], cols), out_dtype, device)
+        _apart(out, x, w, w_scale, bias)
     with _on(device, stream) as handle:
-        y = _output(out, (*x.shape[:-1], cols), out_dtype, device)
-        if out is not None:
-            _apart(out, x, w, w_scale, bias)
-        _, _, y_stride, y_ptr, y_type, _ = m.matrix(y, "out")
-        nbytes = lib.relkl_linear_i8_bytes(rows, K)
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-        ws = _record(device, ws)
-        check(lib.relkl_linear_i8(rows, cols, K, x_ptr, x_type, stride, w_ptr, w_stride, s, b, y_ptr,
-                                  y_type, y_stride, None if scratch is None else scratch.data_ptr(),
-                                  nbytes, ws.data_ptr(), ws.numel(), handle), "relkl_linear_i8")
+        status, y = m.linear_i8(x, w, w_scale, bias, out_dtype, out, _record(device, ws), handle)
+    check(status, "relkl_linear_i8")
     if out is not None:
         m.written([out])
     return y

@@ -94,23 +94,19 @@ def relkl_grad_norm(grads: Sequence[torch.Tensor], max_norm: float = math.inf, *
     together, and the factor min(1, max_norm / (norm + 1e-6)) that clips them to
     ``max_norm`` (NaN where the norm is not finite, as with an element from 2^64 on), for
     relkl_adamw's ``grad_scale``."""
-    n = len(grads)
-    index, table = _abi.marshal().norm(grads)
-    device = grads[0].device
+    marshal = _abi.marshal()
+    index, table = marshal.norm(grads)
+    first = grads[0]
     if out is not None and (out.dtype != torch.float32 or tuple(out.shape) != (2,) or
                             not out.is_contiguous() or out.get_device() != index):
         raise ValueError("out must be a contiguous float32 tensor of two numbers on the "
                          "gradients' device")
-    lib = _abi.lib()
-    nbytes = lib.relkl_grad_norm_bytes(n)
-    with _on(device, stream) as handle:
-        if out is None:
-            out = torch.empty(2, dtype=torch.float32, device=device)
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        check(lib.relkl_grad_norm(n, table, max_norm, out.data_ptr(), scratch.data_ptr(), nbytes,
-                                  handle), "relkl_grad_norm")
-    _abi.marshal().written([out])
-    return out
+    with _on(first.device, stream) as handle:
+        status, got = marshal.grad_norm(first, table, max_norm, out, handle)
+    check(status, "relkl_grad_norm")
+    if out is not None:
+        marshal.written([out])
+    return got
 
 
 class AdamW:

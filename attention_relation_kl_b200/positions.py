@@ -103,14 +103,12 @@ def relkl_rotary_qkv(xs: Sequence[torch.Tensor], inv_freq: torch.Tensor, *,
     elif out_dtype is not None and any(y.dtype != out_dtype for y in out):
         raise ValueError(f"out must be {out_dtype} tensors")
     with _on(x0.device, stream) as handle:
-        given = out is not None
-        out = list(out) if given else [torch.empty(x.shape, dtype=out_dtype, device=x0.device) for x in xs]
-        tensors, plan = marshal.rotary(xs, out, apply, inv_freq, positions, interleaved, inverse,
-                                       mscale, pos_scale, pos_offset)
-        check(_abi.lib().relkl_rotary(len(out), tensors, plan, handle), "relkl_rotary")
-    if given:
-        marshal.written(out)
-    return out
+        status, got = marshal.rotary(xs, out, out_dtype, apply, inv_freq, positions, interleaved, inverse,
+                                     mscale, pos_scale, pos_offset, handle)
+    check(status, "relkl_rotary")
+    if out is not None:
+        marshal.written(got)
+    return got
 
 
 def relkl_rotary(x: torch.Tensor, inv_freq: torch.Tensor, *, pos_scale: float = 1.0,
