@@ -339,6 +339,58 @@ relkl_status build_simt(int32_t n_rel, const relkl_desc* descs, const void* cons
   return RELKL_OK;
 }
 
+// ---- rotary positions
+// A difference of two rows' indices in one direction: lo..hi steps.
+struct Steps {
+  int64_t stride, lo, hi;
+};
+
+// Whether numbers of steps exist whose sum lies in [from, to].  Steps come by
+// falling stride, so few numbers of one leave the rest in reach (one or two,
+// where both tensors have the same strides); `left` bounds the search, and what
+// it does not settle counts as found.
+bool steps_reach(const Steps* s, int n, int64_t from, int64_t to, int& left) {
+  if (n == 0) return from <= 0 && to >= 0;
+  int64_t least = 0, most = 0;      // of the steps behind this one
+  for (int k = 1; k < n; ++k) {
+    least += s[k].lo * s[k].stride;
+    most += s[k].hi * s[k].stride;
+  }
+  auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0); };
+  const int64_t first = std::max(s->lo, -floor_div(most - from, s->stride));
+  const int64_t last = std::min(s->hi, floor_div(to - least, s->stride));
+  for (int64_t m = first; m <= last; ++m) {
+    if (--left < 0) return true;
+    if (steps_reach(s + 1, n - 1, from - m * s->stride, to - m * s->stride, left)) return true;
+  }
+  return false;
+}
+
+// Whether two outputs of a call have an element in common; b begins `apart`
+// elements behind a.
+bool rows_meet(const RotaryTensor& a, const RotaryTensor& b, const relkl_rotary_plan& plan, int64_t apart) {
+  Steps s[6];
+  int n = 0;
+  const int64_t ea[3] = {plan.B, a.H, plan.N}, eb[3] = {plan.B, b.H, plan.N};
+  auto add = [&](int64_t stride, int64_t lo, int64_t hi) {
+    if (stride == 0) return;        // one row only
+    for (int k = 0; k < n; ++k)
+      if (s[k].stride == stride) {
+        s[k].lo += lo;
+        s[k].hi += hi;
+        return;
+      }
+    s[n++] = Steps{stride, lo, hi};
+  };
+  for (int i = 0; i < 3; ++i) {
+    add(a.ys[i], 0, ea[i] - 1);
+    add(b.ys[i], 1 - eb[i], 0);
+  }
+  std::sort(s, s + n, [](const Steps& x, const Steps& y) { return x.stride > y.stride; });
+  int left = 20000;
+  return steps_reach(s, n, apart - (plan.d - 1), apart + (plan.d - 1), left);
+}
+
 // ---- products in 8-bit integers
 constexpr int64_t kMostStride = int64_t(1) << 48;   // keeps every offset far below 2^63
 
@@ -796,11 +848,14 @@ relkl_status relkl_rotary(int32_t n_tensors, const relkl_rotary_tensor* tensors,
     ++p.n;
   }
   if (p.n == 0) return RELKL_OK;
-  // Tensors that are parts of one buffer interleave their ranges, so ranges
-  // are held against each other only where an x meets a y, and not where both
-  // tensors are rotated in place.
+  // Tensors that are parts of one buffer interleave their ranges, so where two
+  // outputs' ranges meet their rows decide.  That settles two tensors rotated
+  // in place too; elsewhere the range of an x may not meet that of a y.
   for (int i = 0; i < p.n; ++i)
     for (int j = 0; j < p.n; ++j) {
+      if (j < i && range[i].y0 < range[j].y1 && range[j].y0 < range[i].y1 &&
+          rows_meet(p.t[i], p.t[j], a, (range[j].y0 - range[i].y0) / ys))
+        return RELKL_ERR_INVALID;
       if (range[i].in_place && range[j].in_place) continue;
       if (range[i].x0 < range[j].y1 && range[j].y0 < range[i].x1) return RELKL_ERR_INVALID;
     }

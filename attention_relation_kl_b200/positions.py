@@ -89,8 +89,9 @@ def relkl_rotary_qkv(xs: Sequence[torch.Tensor], inv_freq: torch.Tensor, *,
     (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``.  ``inverse`` turns back: the
     gradient of the input from that of the output.  ``apply[r] = False`` only moves
     tensor r to its output's layout and type.  ``out`` may have any non-overlapping
-    strides and may be the inputs themselves; without it the outputs are contiguous
-    tensors of ``out_dtype`` (default: the inputs' type)."""
+    strides and may be the inputs themselves, but no element of it is written twice: a
+    tensor given twice is refused as ``out``, in place too; without it the outputs are
+    contiguous tensors of ``out_dtype`` (default: the inputs' type)."""
     marshal = _abi.marshal()
     marshal.rotary_inputs(xs, inv_freq)
     if apply is not None and len(apply) != len(xs) or out is not None and len(out) != len(xs):

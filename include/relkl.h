@@ -374,7 +374,10 @@ typedef struct {
  * long contexts and their factor are the caller's (inv_freq, mscale).
  * Tensors may have any strides whose elements of y do not overlap.  y may be x
  * itself, with the same strides and type (the rotation in place); any other
- * overlap of an x with a y is refused, as far as their address ranges tell.
+ * overlap of an x with a y is refused, as far as their address ranges tell, and
+ * so are two tensors' outputs that have an element in common (parts of one
+ * buffer, rows beside rows, have none; outputs in one buffer at so unlike
+ * strides that a bounded search does not settle it are refused too).
  * inv_freq is 8-byte aligned, positions to its type.  1 <= d <= 512;
  * B, N, H >= 0 (zero work is a no-op).  RELKL_ERR_INVALID for anything else.
  * Any alignment that the types allow is taken; strides and bases that are

@@ -322,3 +322,41 @@ def test_given_outputs_are_seen_as_changed_in_place():
     rk.relkl_rotary(x, f, out=x)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+def test_outputs_are_written_once():
+    # any two outputs in one buffer: taken exactly where no element is in both
+    f, gen = rk.rotary_freqs(4).inv_freq, np.random.default_rng(5)
+    counts = {True: 0, False: 0}
+    for case in range(400):
+        B, N, d = int(gen.integers(1, 4)), int(gen.integers(1, 5)), int(gen.integers(4, 7))
+        buf = torch.zeros(6000, device="cuda")
+        outs, places = [], []
+        inner = int(gen.integers(1, 4)) * d            # the heads' distance in interleaved parts
+        for r in range(int(gen.integers(2, 4))):
+            H = int(gen.integers(1, 4))
+            order = gen.permutation(3) if case % 2 else np.array([1, 2, 0])
+            stride, reach = [0, 0, 0], d if case % 2 else inner
+            for o in order:                            # each step passes what the smaller ones reach
+                stride[o] = reach + (int(gen.integers(0, 9)) if case % 2 else 0)
+                reach = stride[o] * (B, 3 if case % 2 == 0 else H, N)[o]
+            at = int(gen.integers(0, 60 * d))
+            y = buf.as_strided((B, H, N, d), (*stride, 1), at)
+            outs.append(y)
+            places.append(set(torch.arange(6000).as_strided(y.shape, y.stride(), at).flatten().tolist()))
+        free = all(not (a & b) for i, a in enumerate(places) for b in places[:i])
+        counts[free] += 1
+        xs = [_randn(y.shape, F32, case) for y in outs]
+        if free:
+            rk.relkl_rotary_qkv(xs, f, out=outs)
+            for x, y in zip(xs, outs):
+                assert torch.equal(y, rk.relkl_rotary(x, f))
+        else:
+            with pytest.raises(RuntimeError, match="INVALID"):
+                rk.relkl_rotary_qkv(xs, f, out=outs)
+            assert not buf.any()
+    assert min(counts.values()) > 40
+    x, f = _randn((1, 2, 9, 64), F32, 1), rk.rotary_freqs(64).inv_freq
+    q = _randn((1, 4, 9, 64), F32, 2)
+    with pytest.raises(RuntimeError, match="INVALID"):     # a layer that shares K and V
+        rk.relkl_rotary_qkv([q, x, x], f, apply=(True, True, False), out=[q, x, x])

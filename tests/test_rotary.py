@@ -77,6 +77,25 @@ def test_counts_null_arguments_and_crossing_tensors_are_refused():
     assert _call(plan, _tensor(), _tensor(x=2 * FAKE, y=FAKE + 512)) == inv
 
 
+X, Y, ST = FAKE, 16 * FAKE, (1024, 512, 64)
+
+
+@pytest.mark.parametrize("tensors", [
+    [dict(y=X), dict(y=X)],                              # one tensor in place twice
+    [dict(y=X), dict(y=X, apply=0)],                     # turned, and moved onto itself
+    [dict(y=X), dict(x=X + 128, y=X + 128)],             # in place, a row further
+    [dict(y=X), dict(x=X + 2 * 1024, y=X + 2 * 1024)],   # in place, a head further
+    [dict(), dict(x=2 * X)],                             # two inputs, one output
+    [dict(), dict(x=2 * X, y=Y + 2)],                    # ... an element further
+    [dict(), dict(x=2 * X, y=Y + 2 * 2047)],             # the last element of the one, the first of the other
+    [dict(), dict(x=2 * X, y=3 * Y), dict(x=4 * X)],     # the first and the third
+    [dict(ys=(4096, 64, 512)), dict(x=2 * X, ys=(4096, 64, 512), y=Y + 2 * 63)],   # beside, one short
+    [dict(), dict(x=2 * X, H=1, ys=(2048, 0, 256), y=Y + 2 * 64)],    # at other strides
+])
+def test_outputs_with_an_element_in_common_are_refused(tensors):
+    assert _call(_plan(), *[_tensor(**t) for t in tensors]) == _abi.RELKL_ERR_INVALID
+
+
 def test_no_work_is_a_no_op():
     assert _call(_plan(B=0), _tensor(x=None, y=None)) == _abi.RELKL_OK
     assert _call(_plan(N=0), _tensor(x=None, y=None)) == _abi.RELKL_OK
