@@ -248,7 +248,8 @@ __device__ __forceinline__ float root_of(float v) {
   return r;
 }
 __device__ __forceinline__ float moved_fast(const Hyper& h, float p, float m, float root) {
-  float inv;   // the denominator is 0 or a normal number: a root of a float is
+  // the denominator is 0 or a normal number: a root of a float is, and eps is held to that
+  float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(root, h.rbc2, h.eps)));
   return fmaf(p, h.decay, -h.step * (m * inv));
 }

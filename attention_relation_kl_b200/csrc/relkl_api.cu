@@ -4,6 +4,7 @@
 // and a per-device SM-count cache).
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -894,6 +895,10 @@ relkl_status relkl_adamw(int32_t n_tensors, const relkl_adamw_tensor* tensors,
   if (a.step_dev ? !aligned(a.step_dev, 8) : a.step < 1) return RELKL_ERR_INVALID;
   if (!aligned(a.grad_scale, 4)) return RELKL_ERR_INVALID;
   const bool bits8 = a.state_bits == 8;
+  // an eps that float32 does not hold would be 0, and 0 / 0 where m and v are 0;
+  // the reciprocal of the 8-bit kernel takes a subnormal number for 0 as well
+  const float eps = static_cast<float>(a.eps);
+  if (a.eps > 0.0 && (eps == 0.0f || (bits8 && eps < FLT_MIN))) return RELKL_ERR_INVALID;
   for (int32_t k = 0; k < n_tensors; ++k) {
     const relkl_adamw_tensor& t = tensors[k];
     if (t.n < 0 || t.n > (int64_t(1) << 40) || t.reserved != 0 || !number(t.weight_decay))

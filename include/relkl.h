@@ -420,7 +420,9 @@ typedef struct {
   int32_t reserved;      /* must be 0                                         */
   double lr;             /* finite, >= 0                                      */
   double beta1, beta2;   /* in [0, 1)                                         */
-  double eps;            /* finite, >= 0                                      */
+  double eps;            /* finite; 0, or a number above 0 in float32, with states of 8
+                          * bits at least 2^-126.  With 0 an element whose m and v are 0
+                          * becomes NaN, as the formula's 0 / 0                */
   int64_t step;          /* t >= 1: the number of this step                   */
   /* Values that a captured graph takes anew at each replay (DEVICE, or NULL
    * for the ones above).  *step_dev >= 1.                                    */

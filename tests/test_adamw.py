@@ -59,6 +59,11 @@ def test_bad_tensors_are_refused(bits, tensor):
     assert _call(_plan(bits), _tensor(bits, **tensor)) == INV
 
 
+@pytest.mark.parametrize("bits,eps", [(8, 2.0 ** -127), (8, 1e-40), (8, 1e-45), (8, 1e-60), (32, 1e-60)])
+def test_an_eps_that_the_kernel_would_take_for_zero_is_refused(bits, eps):
+    assert _call(_plan(bits, eps=eps), _tensor(bits)) == INV
+
+
 def test_the_same_tensor_twice_is_refused():
     t, u = _tensor(), _tensor(at=16 * FAKE)
     assert _call(_plan(), t, u, t) == INV

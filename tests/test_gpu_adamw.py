@@ -480,3 +480,17 @@ def test_many_elements_and_their_pieces(pt, gt, copies):
         assert torch.equal(x[0], y[0]) and torch.equal(x[3], y[3])
         for a, b in zip(x[2], y[2]):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("bits,eps", [(32, 1e-40), (32, 2.0 ** -126), (8, 2.0 ** -126)])
+def test_the_smallest_eps_leaves_elements_without_moments(bits, eps):
+    p = torch.ones(300, device="cuda")
+    g = torch.zeros(300, device="cuda")
+    g[7] = 1e-3
+    rk.relkl_adamw([p], [g], [rk.adamw_state(p, bits)], lr=1e-3, step=1, eps=eps, weight_decay=0.0)
+    # lr g / (|g| + eps): fourteen roundings of the step, and the weight's own
+    assert abs(float(p[7]) - (1 - 1e-3)) <= 14 * U * 1e-3 + 2.5 * U
+    p[7] = 1.0
+    assert torch.equal(p, torch.ones_like(p))
+    with pytest.raises(RuntimeError):
+        rk.relkl_adamw([p], [g], [rk.adamw_state(p, 8)], lr=1e-3, step=1, eps=1e-40)
