@@ -1184,8 +1184,10 @@ template <typename T, typename U, int R>
 cudaError_t gemv(const GemvParams& p, int num_sms, cudaStream_t stream) {
   const int smem = p.rows * ((p.K + 15) / 16 * 16);
   cudaError_t e = cudaSuccess;
+  // the most that any call takes, not this one's: the limit is the process's, and
+  // another thread's launch may come between a smaller one and its own
   if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(relkl_gemv_i8_kernel<T, U, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(relkl_gemv_i8_kernel<T, U, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemvBytes);
   if (e != cudaSuccess) return e;
   // as many CTAs as the SMs hold at a time: more would code the rows once more
   const int need = (p.cols + GEMV_THREADS / 32 - 1) / (GEMV_THREADS / 32);

@@ -5,6 +5,8 @@ a 31-bit and a 24-bit number that is no half differs from every half by 2^-26 of
 Sums are exact integers; with u = 2^-24 a result rounds the sum, the token's scale, the
 product of the scales and the last sum: 4 u |sum sx sw| + u |bias|, plus 2^-8 in bf16.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -337,3 +339,32 @@ def test_given_outputs_are_seen_as_changed_in_place():
         call(out)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.backward()
+
+
+def test_few_long_rows_from_two_threads():
+    # codes of 48 to 96 KB in shared memory, of other sizes in each thread
+    work = []
+    for k, (rows, K) in enumerate([(4, 24000), (4, 13000)]):
+        w, sw = _weights(8, K, k)
+        x = _randn((rows, K), BF16, 10 + k)
+        work.append((x, w, sw, rk.relkl_linear_i8(x, w, sw)))
+    go, failed = threading.Barrier(2), []
+
+    def calls(x, w, sw, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                go.wait(60)
+                for _ in range(3000):
+                    y = rk.relkl_linear_i8(x, w, sw)
+                torch.cuda.current_stream().synchronize()
+                assert torch.equal(y, want)
+        except Exception as e:      # seen by the test's own thread
+            failed.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=calls, args=a) for a in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
