@@ -15,6 +15,7 @@
 namespace relkl {
 
 constexpr int SB = 32;           // rows per block and columns per tile
+constexpr int SIMT_MOST_D = 128;   // the largest head that this path takes
 constexpr int SIMT_THREADS = 256;  // 32 rows x 8 column groups of 4
 
 __device__ __forceinline__ float load_x(const void* base, int is_bf16, int64_t off) {
@@ -185,7 +186,7 @@ relkl_bwd_simt_kernel(const __grid_constant__ SimtParams p) {
     if (p.causal ? row == 0 : U.L == 1) mul = 0.f;
   }
   // dX_I accumulator: this thread owns columns cg, cg+8, ... of row rr
-  constexpr int MAXC = 128 / 8;
+  constexpr int MAXC = SIMT_MOST_D / 8;
   float acc[MAXC];
 #pragma unroll
   for (int m = 0; m < MAXC; ++m) acc[m] = 0.f;
@@ -257,9 +258,11 @@ static size_t simt_smem(int d, int bwd) {
 cudaError_t simt_launch_fwd(const SimtParams& p, cudaStream_t stream) {
   if (p.n_units * p.nblk_local == 0) return cudaSuccess;
   const size_t sm = simt_smem(p.d, 0);
+  // the limit is the process's: not this call's size, which another thread's
+  // larger call may meet between its own setting and its launch
   cudaError_t e = cudaFuncSetAttribute(relkl_fwd_simt_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(sm));
+                                       static_cast<int>(simt_smem(SIMT_MOST_D, 0)));
   if (e != cudaSuccess) return e;
   relkl_fwd_simt_kernel<<<p.n_units * p.nblk_local, SIMT_THREADS, sm, stream>>>(p);
   return cudaGetLastError();
@@ -270,7 +273,7 @@ cudaError_t simt_launch_bwd(const SimtParams& p, cudaStream_t stream) {
   const size_t sm = simt_smem(p.d, 1);
   cudaError_t e = cudaFuncSetAttribute(relkl_bwd_simt_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(sm));
+                                       static_cast<int>(simt_smem(SIMT_MOST_D, 1)));
   if (e != cudaSuccess) return e;
   relkl_bwd_simt_kernel<<<p.n_units * p.nblk_local, SIMT_THREADS, sm, stream>>>(p);
   return cudaGetLastError();
