@@ -23,7 +23,7 @@ EXPORTS = ("relkl_workspace_bytes", "relkl_workspace_init", "relkl_fwd", "relkl_
            "relkl_path_for", "relkl_fwd_noalloc", "relkl_rope_bwd", "relkl_weight_grad",
            "relkl_cast_bf16", "relkl_bwd_kernel_for",
            "relkl_fwd_qkv_part", "relkl_bwd_qkv_part", "relkl_check_schedule",
-           "relkl_rotary", "relkl_adamw", "relkl_grad_norm", "relkl_grad_norm_bytes",
+           "relkl_rotary", "relkl_adamw", "relkl_adamw_check", "relkl_grad_norm", "relkl_grad_norm_bytes",
            "relkl_quantize_rows", "relkl_matmul_i8", "relkl_linear_i8", "relkl_linear_i8_bytes")
 
 
@@ -135,6 +135,8 @@ def _declare(lib):
     lib.relkl_rotary.argtypes = [i32, _vp, _vp, _vp]   # arrays of the structs, or their bytes
     lib.relkl_adamw.restype = ctypes.c_int
     lib.relkl_adamw.argtypes = [i32, _vp, _vp, _vp]
+    lib.relkl_adamw_check.restype = ctypes.c_int
+    lib.relkl_adamw_check.argtypes = [i32, _vp, _vp]
     lib.relkl_grad_norm_bytes.restype = ctypes.c_size_t
     lib.relkl_grad_norm_bytes.argtypes = [i32]
     lib.relkl_grad_norm.restype = ctypes.c_int

@@ -21,7 +21,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "librelkl.so")
 SOURCES = ["relkl_api.cu", "relkl_tc.cu", "relkl_simt.cu", "relkl_chain.cu", "relkl_gemm.cu",
            "relkl_rotary.cu", "relkl_adamw.cu", "relkl_int8.cu"]
-HEADERS = ["relkl_device.cuh", "relkl_params.h"]
+HEADERS = ["relkl_device.cuh", "relkl_params.h", "relkl_ranges.h"]
 MARSHAL_SOURCE = os.path.join(CSRC, "relkl_marshal.cpp")
 MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 
@@ -60,7 +60,8 @@ def _run(cmd, verbose: bool) -> None:
 
 def build_marshal(force: bool = False, verbose: bool = False) -> str:
     """Compile the marshalling module if its sources are newer; returns its path."""
-    deps = [MARSHAL_SOURCE, os.path.join(ROOT, "include", "relkl.h"), __file__]
+    deps = [MARSHAL_SOURCE, os.path.join(CSRC, "relkl_ranges.h"), os.path.join(ROOT, "include", "relkl.h"),
+            __file__]
     if not force and os.path.exists(MARSHAL) and \
             all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
         return MARSHAL

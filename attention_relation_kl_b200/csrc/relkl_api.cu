@@ -19,6 +19,7 @@
 #include "../../include/relkl.h"
 #include "relkl_device.cuh"
 #include "relkl_params.h"
+#include "relkl_ranges.h"
 
 namespace relkl {
 cudaError_t tc_launch_fwd(const TcParams& p, int d, int grid, cudaStream_t stream);
@@ -882,9 +883,8 @@ relkl_status relkl_rotary(int32_t n_tensors, const relkl_rotary_tensor* tensors,
   return e == cudaSuccess ? RELKL_OK : cuda_fail(e);
 }
 
-relkl_status relkl_adamw(int32_t n_tensors, const relkl_adamw_tensor* tensors,
-                         const relkl_adamw_plan* plan, void* stream) {
-  NvtxRange nvtx_range("relkl_adamw");
+relkl_status relkl_adamw_check(int32_t n_tensors, const relkl_adamw_tensor* tensors,
+                               const relkl_adamw_plan* plan) {
   if (n_tensors < 0 || !plan || (n_tensors > 0 && !tensors)) return RELKL_ERR_INVALID;
   const relkl_adamw_plan& a = *plan;
   if ((a.state_bits != 32 && a.state_bits != 8) || a.reserved != 0) return RELKL_ERR_INVALID;
@@ -916,6 +916,26 @@ relkl_status relkl_adamw(int32_t n_tensors, const relkl_adamw_tensor* tensors,
               : (t.m_scale || t.v_scale))
       return RELKL_ERR_INVALID;
   }
+  for (int32_t k = 0; k < n_tensors;) {   // by launches
+    Range range[kAdamwRanges * kAdamwMost];
+    int n = 0, nr = 0;
+    for (; k < n_tensors && n < kAdamwMost; ++k) {
+      if (tensors[k].n == 0) continue;
+      nr += adamw_ranges(tensors[k], bits8, range + nr);
+      ++n;
+    }
+    if (overlaps(range, nr)) return RELKL_ERR_INVALID;
+  }
+  return RELKL_OK;
+}
+
+relkl_status relkl_adamw(int32_t n_tensors, const relkl_adamw_tensor* tensors,
+                         const relkl_adamw_plan* plan, void* stream) {
+  NvtxRange nvtx_range("relkl_adamw");
+  const relkl_status refused = relkl_adamw_check(n_tensors, tensors, plan);
+  if (refused != RELKL_OK) return refused;
+  const relkl_adamw_plan& a = *plan;
+  const bool bits8 = a.state_bits == 8;
   AdamwPlan p;
   p.lr = a.lr;
   p.bc1 = 1.0 - std::pow(a.beta1, static_cast<double>(a.step));
@@ -932,65 +952,32 @@ relkl_status relkl_adamw(int32_t n_tensors, const relkl_adamw_tensor* tensors,
   p.lr_dev = a.lr_dev;
   p.step_dev = reinterpret_cast<const long long*>(a.step_dev);
   p.grad_scale = a.grad_scale;
-  // One launch's arrays by address: a written one overlaps none.
-  struct Range { uintptr_t begin, end; bool written; };
-  auto add = [](Range* r, int& n, const void* x, int64_t bytes, bool written) {
-    if (!x) return;
-    const uintptr_t b = reinterpret_cast<uintptr_t>(x);
-    r[n++] = Range{b, b + static_cast<uintptr_t>(bytes), written};
-  };
-  auto overlaps = [](Range* r, int n) {
-    std::sort(r, r + n, [](const Range& x, const Range& y) { return x.begin < y.begin; });
-    uintptr_t read = 0, written = 0;   // the ends so far
-    for (int i = 0; i < n; ++i) {
-      if (r[i].begin < written || (r[i].written && r[i].begin < read)) return true;
-      uintptr_t& end = r[i].written ? written : read;
-      end = r[i].end > end ? r[i].end : end;
+  for (int32_t k = 0; k < n_tensors;) {
+    AdamwTensor group[kAdamwMost];
+    int n = 0;
+    for (; k < n_tensors && n < kAdamwMost; ++k) {
+      const relkl_adamw_tensor& t = tensors[k];
+      if (t.n == 0) continue;
+      const bool gb = t.grad_dtype == RELKL_BF16, pb = t.param_dtype == RELKL_BF16;
+      AdamwTensor& g = group[n++];
+      g.grad = t.grad;
+      g.param = t.param;
+      g.copy = t.copy;
+      g.m = t.m;
+      g.v = t.v;
+      g.m_scale = t.m_scale;
+      g.v_scale = t.v_scale;
+      g.n = t.n;
+      g.weight_decay = t.weight_decay;
+      g.decay = static_cast<float>(1.0 - a.lr * static_cast<double>(t.weight_decay));
+      g.grad_bf16 = gb;
+      g.param_bf16 = pb;
+      g.wide = aligned(t.grad, gb ? 8 : 16) && aligned(t.param, pb ? 8 : 16) &&
+               aligned(t.copy, 8) && aligned(t.m, bits8 ? 8 : 16) && aligned(t.v, bits8 ? 8 : 16);
     }
-    return false;
-  };
-  // Twice over the call's launches: every check comes before the first launch.
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int32_t k = 0; k < n_tensors;) {
-      AdamwTensor group[kAdamwMost];
-      Range range[7 * kAdamwMost];
-      int n = 0, nr = 0;
-      for (; k < n_tensors && n < kAdamwMost; ++k) {
-        const relkl_adamw_tensor& t = tensors[k];
-        if (t.n == 0) continue;
-        const bool gb = t.grad_dtype == RELKL_BF16, pb = t.param_dtype == RELKL_BF16;
-        const int64_t blocks = (t.n + 255) / 256, ss = bits8 ? 1 : 4;
-        if (pass == 0) {
-          add(range, nr, t.grad, t.n * (gb ? 2 : 4), false);
-          add(range, nr, t.param, t.n * (pb ? 2 : 4), true);
-          add(range, nr, t.copy, t.n * 2, true);
-          add(range, nr, t.m, t.n * ss, true);
-          add(range, nr, t.v, t.n * ss, true);
-          add(range, nr, t.m_scale, blocks * 4, true);
-          add(range, nr, t.v_scale, blocks * 4, true);
-        }
-        AdamwTensor& g = group[n++];
-        g.grad = t.grad;
-        g.param = t.param;
-        g.copy = t.copy;
-        g.m = t.m;
-        g.v = t.v;
-        g.m_scale = t.m_scale;
-        g.v_scale = t.v_scale;
-        g.n = t.n;
-        g.weight_decay = t.weight_decay;
-        g.decay = static_cast<float>(1.0 - a.lr * static_cast<double>(t.weight_decay));
-        g.grad_bf16 = gb;
-        g.param_bf16 = pb;
-        g.wide = aligned(t.grad, gb ? 8 : 16) && aligned(t.param, pb ? 8 : 16) &&
-                 aligned(t.copy, 8) && aligned(t.m, bits8 ? 8 : 16) && aligned(t.v, bits8 ? 8 : 16);
-      }
-      if (pass == 0) {
-        if (overlaps(range, nr)) return RELKL_ERR_INVALID;
-      } else if (n > 0) {
-        cudaError_t e = launch_adamw(group, n, p, bits8, static_cast<cudaStream_t>(stream));
-        if (e != cudaSuccess) return cuda_fail(e);
-      }
+    if (n > 0) {
+      cudaError_t e = launch_adamw(group, n, p, bits8, static_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return cuda_fail(e);
     }
   }
   return RELKL_OK;

@@ -18,6 +18,7 @@
 #include <torch/csrc/autograd/variable.h>
 
 #include "../../include/relkl.h"
+#include "relkl_ranges.h"
 
 namespace {
 
@@ -215,6 +216,15 @@ PyObject* adamw(PyObject*, PyObject* args) {
       }
       r.weight_decay = static_cast<float>(one_decay ? decay : number(decays[k]));
       (bits8 ? of8 : of32).push_back(r);
+    }
+    if (!of32.empty() && !of8.empty()) {   // two calls, each of which looks at its own arrays
+      std::vector<relkl::Range> ranges(relkl::kAdamwRanges * static_cast<size_t>(n));
+      int64_t count = 0;
+      for (const auto* group : {&of32, &of8})
+        for (const relkl_adamw_tensor& t : *group)
+          count += relkl::adamw_ranges(t, group == &of8, ranges.data() + count);
+      if (relkl::overlaps(ranges.data(), count))
+        raise(PyExc_RuntimeError, "relkl_adamw: a tensor that is written overlaps another one of the call");
     }
     PyObject* groups = PyList_New(0);
     if (!groups) throw Raised{};

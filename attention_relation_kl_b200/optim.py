@@ -79,13 +79,24 @@ def relkl_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         step, step_ptr = 1, _scalar(step, torch.int64, index, "step")
     if grad_scale is not None:
         scale_ptr = _scalar(grad_scale, torch.float32, index, "grad_scale")
+    lib, status, calls = _abi.lib(), _abi.RELKL_OK, 0
     with _on(params[0].device, stream) as handle:
-        for bits, n, table in groups:      # float32 states, then those of 8 bits
-            plan = _PLAN.pack(bits, 0, lr, betas[0], betas[1], eps, step, lr_ptr, step_ptr, scale_ptr)
-            check(_abi.lib().relkl_adamw(n, table, plan, handle), "relkl_adamw")
-    _abi.marshal().written(params)
-    if copies is not None:
-        _abi.marshal().written(copies)
+        # float32 states, then those of 8 bits
+        plans = [_PLAN.pack(bits, 0, lr, betas[0], betas[1], eps, step, lr_ptr, step_ptr, scale_ptr)
+                 for bits, _, _ in groups]
+        if len(groups) > 1:        # all are refused, or none
+            for (_, n, table), plan in zip(groups, plans):
+                check(lib.relkl_adamw_check(n, table, plan), "relkl_adamw")
+        for (_, n, table), plan in zip(groups, plans):
+            status = lib.relkl_adamw(n, table, plan, handle)
+            if status != _abi.RELKL_OK:
+                break
+            calls += 1
+    if calls or status == _abi.RELKL_ERR_CUDA:     # something may have been written
+        _abi.marshal().written(params)
+        if copies is not None:
+            _abi.marshal().written(copies)
+    check(status, "relkl_adamw")
 
 
 def relkl_grad_norm(grads: Sequence[torch.Tensor], max_norm: float = math.inf, *,

@@ -443,6 +443,11 @@ typedef struct {
 relkl_status relkl_adamw(int32_t n_tensors, const relkl_adamw_tensor* tensors,
                          const relkl_adamw_plan* plan, void* stream);
 
+/* What relkl_adamw would refuse, without a step (host only): for a step that is
+ * more than one call, whose tables are all checked before the first.          */
+relkl_status relkl_adamw_check(int32_t n_tensors, const relkl_adamw_tensor* tensors,
+                               const relkl_adamw_plan* plan);
+
 typedef struct {
   const void* grad;
   int64_t n;

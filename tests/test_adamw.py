@@ -73,6 +73,25 @@ def test_the_same_tensor_twice_is_refused():
     assert _call(_plan(), t, u) == INV
 
 
+def test_checks_by_themselves():
+    lib = _abi.lib()
+
+    def refused(plan, *tensors):
+        return lib.relkl_adamw_check(len(tensors), (_abi.relkl_adamw_tensor * max(1, len(tensors)))(*tensors),
+                                     ctypes.byref(plan))
+
+    # taken, on the host: nothing is launched
+    assert refused(_plan(), _tensor(), _tensor(at=16 * FAKE)) == _abi.RELKL_OK
+    assert refused(_plan(8), _tensor(8), _tensor(8, at=16 * FAKE, grad=FAKE)) == _abi.RELKL_OK
+    assert refused(_plan()) == _abi.RELKL_OK
+    for plan, tensors in [(_plan(step=0), [_tensor()]), (_plan(), [_tensor(), _tensor()]),
+                          (_plan(8, eps=1e-40), [_tensor(8)]), (_plan(8), [_tensor()]),
+                          (_plan(), [_tensor(), _tensor(at=16 * FAKE, weight_decay=-1.0)])]:
+        assert refused(plan, *tensors) == INV
+    assert lib.relkl_adamw_check(1, None, ctypes.byref(_plan())) == INV
+    assert lib.relkl_adamw_check(0, None, None) == INV
+
+
 def test_nothing_to_do():
     assert _call(_plan()) == _abi.RELKL_OK
     assert _call(_plan(), _tensor(n=0, grad=None, param=None, m=None, v=None)) == _abi.RELKL_OK

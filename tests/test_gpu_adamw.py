@@ -494,3 +494,32 @@ def test_the_smallest_eps_leaves_elements_without_moments(bits, eps):
     assert torch.equal(p, torch.ones_like(p))
     with pytest.raises(RuntimeError):
         rk.relkl_adamw([p], [g], [rk.adamw_state(p, 8)], lr=1e-3, step=1, eps=1e-40)
+
+
+def test_a_refused_call_of_both_kinds_of_states_changes_nothing():
+    a = _make((300, 4000), 32, F32, F32, 15)
+    b = _make((700, 90), 8, F32, F32, 16)
+    params, grads, states = (list(x) + list(y) for x, y in zip(a[:3], b[:3]))
+    ok = dict(step=3, weight_decay=[0.1] * 4)
+    twice = lambda xs, k: xs + [xs[k]]  # noqa: E731
+    other = rk.AdamWState(*(x.clone() for x in states[0][:2]))
+    whole = params + [y for s in states for y in s if y is not None]
+    before = [x.clone() for x in whole]
+    versions = [p._version for p in params]
+    for args, kw in [
+        ((twice(params, 3), twice(grads, 3), twice(states, 3)), dict(weight_decay=0.1)),
+        ((params, grads, states), dict(weight_decay=[0.1, 0.1, 0.1, -0.1])),
+        ((params, grads, states), dict(eps=1e-40)),      # the 8-bit states' limit
+        # a parameter with a state of each kind, and one tensor's gradient that another writes
+        ((params + [params[3]], grads + [grads[3]], states + [rk.AdamWState(*(
+            torch.zeros(90, device="cuda") for _ in range(2)))]), dict(weight_decay=0.1)),
+        ((params, [params[2][:300], *grads[1:]], states), {}),
+    ]:
+        with pytest.raises(RuntimeError):
+            rk.relkl_adamw(*args, **{**HYPER, **ok, **kw})
+        torch.cuda.synchronize()
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(whole, before))
+        assert [p._version for p in params] == versions
+    # the same gradient twice is read twice
+    rk.relkl_adamw([params[0], params[3]], [grads[0], grads[0][:90]], [other, states[3]], step=3, **HYPER)
+    assert params[0]._version == versions[0] + 1
