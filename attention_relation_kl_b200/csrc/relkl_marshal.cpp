@@ -7,7 +7,9 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <map>
 #include <unordered_set>
+#include <utility>
 #include <vector>
 
 #include <c10/core/impl/VirtualGuardImpl.h>
@@ -141,12 +143,19 @@ double number(PyObject* o) {
   return x;
 }
 
-// adamw(params, grads, states, copies, weight_decay) ->
-//   (device index, [(state bits, count, relkl_adamw_tensor records), ...])
+long long whole(PyObject* o) {
+  const long long x = PyLong_AsLongLong(o);
+  if (x == -1 && PyErr_Occurred()) throw Raised{};
+  return x;
+}
+
+// adamw(params, grads, states, copies, weight_decay, step) ->
+//   (device index, [(state bits, step, count, relkl_adamw_tensor records), ...]): tensors of
+// one kind of states and one step number make a group, float32 states first, then by number
 PyObject* adamw(PyObject*, PyObject* args) {
   return guarded([&]() -> PyObject* {
-    PyObject *ps, *gs, *ss, *cs, *ds;
-    if (!PyArg_ParseTuple(args, "OOOOO", &ps, &gs, &ss, &cs, &ds)) throw Raised{};
+    PyObject *ps, *gs, *ss, *cs, *ds, *ns;
+    if (!PyArg_ParseTuple(args, "OOOOOO", &ps, &gs, &ss, &cs, &ds, &ns)) throw Raised{};
     const Items params(ps, "params must be a sequence"), grads(gs, "grads must be a sequence");
     const Items states(ss, "states must be a sequence");
     const Items copies(cs == Py_None ? ps : cs, "copies must be a sequence");
@@ -158,9 +167,12 @@ PyObject* adamw(PyObject*, PyObject* args) {
     const Items decays(one_decay ? ps : ds, "weight_decay must be a number or a sequence");
     if (decays.size() != n)
       raise(PyExc_ValueError, "weight_decay needs one number, or one for each tensor");
+    const bool one_step = PyIndex_Check(ns) && !PySequence_Check(ns);
+    const long long step = one_step ? whole(ns) : 0;
+    const Items steps(one_step ? ps : ns, "step must be a number or a sequence");
+    if (steps.size() != n) raise(PyExc_ValueError, "step needs one number, or one for each tensor");
     int index = -1;
-    std::vector<relkl_adamw_tensor> of32, of8;
-    (n > 0 ? of32 : of8).reserve(static_cast<size_t>(n));
+    std::map<std::pair<bool, long long>, std::vector<relkl_adamw_tensor>> groups;   // by (8 bits, step)
     for (Py_ssize_t k = 0; k < n; ++k) {
       const at::Tensor& p = tensor(params[k], "params");
       const at::Tensor& g = tensor(grads[k], "gradients");
@@ -215,31 +227,32 @@ PyObject* adamw(PyObject*, PyObject* args) {
         raise(PyExc_ValueError, "float32 states have no scales");
       }
       r.weight_decay = static_cast<float>(one_decay ? decay : number(decays[k]));
-      (bits8 ? of8 : of32).push_back(r);
+      auto& group = groups[{bits8, one_step ? step : whole(steps[k])}];
+      if (groups.size() == 1 && group.empty()) group.reserve(static_cast<size_t>(n));
+      group.push_back(r);
     }
-    if (!of32.empty() && !of8.empty()) {   // two calls, each of which looks at its own arrays
+    if (groups.size() > 1) {   // as many calls, each of which looks at its own arrays
       std::vector<relkl::Range> ranges(relkl::kAdamwRanges * static_cast<size_t>(n));
       int64_t count = 0;
-      for (const auto* group : {&of32, &of8})
-        for (const relkl_adamw_tensor& t : *group)
-          count += relkl::adamw_ranges(t, group == &of8, ranges.data() + count);
+      for (const auto& [key, group] : groups)
+        for (const relkl_adamw_tensor& t : group)
+          count += relkl::adamw_ranges(t, key.first, ranges.data() + count);
       if (relkl::overlaps(ranges.data(), count))
         raise(PyExc_RuntimeError, "relkl_adamw: a tensor that is written overlaps another one of the call");
     }
-    PyObject* groups = PyList_New(0);
-    if (!groups) throw Raised{};
-    for (const auto* group : {&of32, &of8}) {
-      if (group->empty()) continue;
-      PyObject* one = Py_BuildValue("(inN)", group == &of8 ? 8 : 32, static_cast<Py_ssize_t>(group->size()),
-                                    bytes_of(*group));
-      if (!one || PyList_Append(groups, one) != 0) {
+    PyObject* list = PyList_New(0);
+    if (!list) throw Raised{};
+    for (const auto& [key, group] : groups) {
+      PyObject* one = Py_BuildValue("(iLnN)", key.first ? 8 : 32, key.second,
+                                    static_cast<Py_ssize_t>(group.size()), bytes_of(group));
+      if (!one || PyList_Append(list, one) != 0) {
         Py_XDECREF(one);
-        Py_DECREF(groups);
+        Py_DECREF(list);
         throw Raised{};
       }
       Py_DECREF(one);
     }
-    return Py_BuildValue("(iN)", index, groups);
+    return Py_BuildValue("(iN)", index, list);
   });
 }
 

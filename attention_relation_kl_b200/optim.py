@@ -56,7 +56,7 @@ def _scalar(x: torch.Tensor, dtype: torch.dtype, index: int, what: str) -> int:
 
 def relkl_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                 states: Sequence[AdamWState], *, lr: Union[float, torch.Tensor],
-                step: Union[int, torch.Tensor], betas=(0.9, 0.999), eps: float = 1e-8,
+                step: Union[int, Sequence[int], torch.Tensor], betas=(0.9, 0.999), eps: float = 1e-8,
                 weight_decay: Union[float, Sequence[float]] = 0.01,
                 copies: Optional[Sequence[torch.Tensor]] = None,
                 grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -65,29 +65,32 @@ def relkl_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
 
     ``step`` is the number of this step, from 1.  ``lr`` (float32) and ``step`` (int64)
     may be CUDA tensors of one number, read when the work runs, for captured graphs.
-    ``weight_decay`` may give a number for each tensor.  ``copies`` are bf16 tensors
+    ``weight_decay`` and ``step`` may give a number for each tensor (a launch for each
+    number of steps among them).  ``copies`` are bf16 tensors
     that receive the new parameters rounded.  ``grad_scale``, one float32 number on the
     device, multiplies the gradients; where it is not finite nothing is written at all.
     """
     if len(params) == 0 and len(grads) == 0 and len(states) == 0:
         return
-    index, groups = _abi.marshal().adamw(params, grads, states, copies, weight_decay)
     lr_ptr = step_ptr = scale_ptr = 0
+    step_dev = None
+    if isinstance(step, torch.Tensor):
+        step, step_dev = 1, step
+    index, groups = _abi.marshal().adamw(params, grads, states, copies, weight_decay, step)
     if isinstance(lr, torch.Tensor):
         lr, lr_ptr = 0.0, _scalar(lr, torch.float32, index, "lr")
-    if isinstance(step, torch.Tensor):
-        step, step_ptr = 1, _scalar(step, torch.int64, index, "step")
+    if step_dev is not None:
+        step_ptr = _scalar(step_dev, torch.int64, index, "step")
     if grad_scale is not None:
         scale_ptr = _scalar(grad_scale, torch.float32, index, "grad_scale")
     lib, status, calls = _abi.lib(), _abi.RELKL_OK, 0
     with _on(params[0].device, stream) as handle:
-        # float32 states, then those of 8 bits
-        plans = [_PLAN.pack(bits, 0, lr, betas[0], betas[1], eps, step, lr_ptr, step_ptr, scale_ptr)
-                 for bits, _, _ in groups]
+        plans = [_PLAN.pack(bits, 0, lr, betas[0], betas[1], eps, number, lr_ptr, step_ptr, scale_ptr)
+                 for bits, number, _, _ in groups]
         if len(groups) > 1:        # all are refused, or none
-            for (_, n, table), plan in zip(groups, plans):
+            for (_, _, n, table), plan in zip(groups, plans):
                 check(lib.relkl_adamw_check(n, table, plan), "relkl_adamw")
-        for (_, n, table), plan in zip(groups, plans):
+        for (_, _, n, table), plan in zip(groups, plans):
             status = lib.relkl_adamw(n, table, plan, handle)
             if status != _abi.RELKL_OK:
                 break
@@ -126,7 +129,9 @@ class AdamW:
     ``step(grads)`` takes the gradients in the parameters' order (None leaves a parameter as
     it is), or the parameters' ``.grad`` without them; with ``max_norm`` the gradients are
     clipped by the norm of all of them, and a step whose norm is not finite changes nothing
-    but the count.  The count is a host number: for a captured graph call relkl_adamw with
+    but the counts.  ``counts`` holds the steps of each parameter, by which its moments are
+    corrected: those that had a gradient for it; ``steps`` those of any, and setting it sets
+    them all.  The counts are host numbers: for a captured graph call relkl_adamw with
     ``step`` and ``lr`` on the device.
     """
 
@@ -145,6 +150,14 @@ class AdamW:
         self.state = [adamw_state(p, state_bits) for p in self.params]
         self.steps = 0
 
+    @property
+    def steps(self) -> int:
+        return self._steps
+
+    @steps.setter
+    def steps(self, number: int) -> None:
+        self._steps, self.counts = number, [number] * len(self.params)
+
     def step(self, grads: Optional[Sequence[Optional[torch.Tensor]]] = None) -> Optional[torch.Tensor]:
         """Updates the parameters; returns the gradients' norm (on the device) with max_norm."""
         if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
@@ -159,20 +172,27 @@ class AdamW:
         pick = lambda xs: [xs[k] for k in at]  # noqa: E731
         grads = pick(grads)
         clip = None if self.max_norm is None else relkl_grad_norm(grads, self.max_norm)
-        relkl_adamw(pick(self.params), grads, pick(self.state), lr=self.lr, step=self.steps + 1,
+        counts = [self.counts[k] + 1 for k in at]
+        if counts.count(counts[0]) == len(counts):
+            counts = counts[0]
+        relkl_adamw(pick(self.params), grads, pick(self.state), lr=self.lr, step=counts,
                     betas=self.betas, eps=self.eps, weight_decay=pick(self.weight_decay),
                     copies=None if self.copies is None else pick(self.copies),
                     grad_scale=None if clip is None else clip[1:])
-        self.steps += 1
+        self._steps += 1
+        for k in at:
+            self.counts[k] += 1
         return None if clip is None else clip[0]
 
     def state_dict(self) -> dict:
-        return {"steps": self.steps, "state": [tuple(s) for s in self.state]}
+        return {"steps": self.steps, "counts": list(self.counts), "state": [tuple(s) for s in self.state]}
 
     def load_state_dict(self, saved: dict) -> None:
-        """Copies a state_dict's values into this optimizer's states (which keep their place)."""
-        states = saved["state"]
-        if len(states) != len(self.state):
+        """Copies a state_dict's values into this optimizer's states (which keep their place).
+        One without ``counts`` has the same count for all parameters."""
+        states, steps = saved["state"], int(saved["steps"])
+        counts = [int(c) for c in saved.get("counts", [steps] * len(states))]
+        if len(states) != len(self.state) or len(counts) != len(states):
             raise ValueError("the saved state is of another number of parameters")
         for mine, theirs in zip(self.state, states):
             for a, b in zip(mine, theirs):
@@ -182,4 +202,4 @@ class AdamW:
             for a, b in zip(mine, theirs):
                 if a is not None:
                     a.copy_(b)
-        self.steps = int(saved["steps"])
+        self._steps, self.counts = steps, counts

@@ -167,3 +167,25 @@ def test_optimizer_state_round_trip_on_the_host():
     with pytest.raises(ValueError):
         a.step([None])
     assert a.step() is None and a.steps == 7      # no gradient, no step
+
+
+def test_counts_of_each_parameter():
+    p = [torch.zeros(300), torch.zeros(2, 2)]
+    a, b = rk.AdamW(p), rk.AdamW(p)
+    assert a.counts == [0, 0]
+    a.steps = 5                                   # of all of them
+    assert a.counts == [5, 5] and a.steps == 5
+    a.counts[1] = 3
+    b.load_state_dict(a.state_dict())
+    assert b.steps == 5 and b.counts == [5, 3]
+    b.counts[0] = 9
+    assert a.counts == [5, 3]
+    old = {k: v for k, v in a.state_dict().items() if k != "counts"}
+    b.load_state_dict(old)                        # saved without counts
+    assert b.counts == [5, 5]
+    with pytest.raises(ValueError):
+        b.load_state_dict({**a.state_dict(), "counts": [1]})
+    s = [rk.adamw_state(x) for x in p]
+    for bad in ([1], [1, 2, 3], [1, "a"], 1.0, None):
+        with pytest.raises((TypeError, ValueError)):
+            rk.relkl_adamw(p, p, s, lr=1e-3, step=bad)

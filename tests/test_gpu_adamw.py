@@ -523,3 +523,48 @@ def test_a_refused_call_of_both_kinds_of_states_changes_nothing():
     # the same gradient twice is read twice
     rk.relkl_adamw([params[0], params[3]], [grads[0], grads[0][:90]], [other, states[3]], step=3, **HYPER)
     assert params[0]._version == versions[0] + 1
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_moments_are_corrected_by_each_parameters_own_steps(bits):
+    params, grads, _, copies = _make((400, 64, 3000), bits, F32, F32, 17, copies=True)
+    decay = [0.1, 0.0, 0.2]
+    opt = rk.AdamW(params, weight_decay=decay, state_bits=bits, copies=copies, **HYPER)
+    for t, with_gradient in enumerate([(0, 2), (0, 2), (0, 1, 2), (1,), (0, 1, 2)]):
+        want = {k: Expected(params[k], grads[k], opt.state[k], opt.counts[k] + 1, HYPER["lr"], *HYPER["betas"],
+                            HYPER["eps"], decay[k]) for k in with_gradient}
+        opt.step([g if k in with_gradient else None for k, g in enumerate(grads)])
+        for k, w in want.items():
+            w.check(params[k], opt.state[k], copies[k])
+        assert opt.steps == t + 1
+    assert opt.counts == [4, 3, 4]
+    # the first step of a parameter goes lr along its gradient's sign, whenever it comes
+    p = [torch.zeros(8, device="cuda"), torch.zeros(8, device="cuda")]
+    late = rk.AdamW(p, weight_decay=0.0, state_bits=bits, **HYPER)
+    one = torch.ones(8, device="cuda")
+    for _ in range(10):
+        late.step([one, None])
+    late.step([one, one])
+    assert np.all(np.abs(_f64(p[1]) + HYPER["lr"]) <= HYPER["lr"] * (14 * U + HYPER["eps"]))
+
+
+def test_steps_given_for_each_tensor():
+    a = _make((300, 4000, 17), 32, F32, F32, 18)
+    b = _make((700, 90), 8, F32, F32, 19)
+    params, grads, states = (list(x) + list(y) for x, y in zip(a[:3], b[:3]))
+    steps = [7, 1, 7, np.int64(1), 12]
+    want = [Expected(p, g, s, int(t), HYPER["lr"], *HYPER["betas"], HYPER["eps"], 0.1)
+            for p, g, s, t in zip(params, grads, states, steps)]
+    rk.relkl_adamw(params, grads, states, step=steps, weight_decay=0.1, **HYPER)
+    for w, p, s in zip(want, params, states):
+        w.check(p, s)
+    whole = params + [y for s in states for y in s if y is not None]
+    before = [x.clone() for x in whole]
+    for bad in (dict(step=[7, 1, 7, 1, 0]), dict(step=[1, 2, 1, 1, 1], weight_decay=[0, 0, 0, 0, -1.0])):
+        with pytest.raises(RuntimeError):
+            rk.relkl_adamw(params, grads, states, **{"weight_decay": 0.1, **HYPER, **bad})
+    # one tensor at two numbers of steps
+    with pytest.raises(RuntimeError, match="overlaps"):
+        rk.relkl_adamw(params[:1] * 2, grads[:1] * 2, states[:1] * 2, step=[1, 2], **HYPER)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(whole, before))
