@@ -94,9 +94,14 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 class _on:
     """Makes ``device`` current, and ``stream`` (a torch stream or a cudaStream_t
     handle) if one is given, so that what a call allocates for itself belongs to
-    the stream that uses it.  Enters as the cudaStream_t handle."""
+    the stream that uses it.  Enters as the cudaStream_t handle.  A torch stream
+    of another device is refused: making it current would leave the call's work on
+    a stream that was not asked for, under the wrong device."""
 
     def __init__(self, device: torch.device, stream=None):
+        where = getattr(stream, "device", None)
+        if isinstance(where, torch.device) and where != device:
+            raise ValueError(f"stream is on {where}, the tensors are on {device}")
         self.device, self.stream, self.inner = device, stream, None
 
     def __enter__(self) -> int:

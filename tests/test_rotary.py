@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import attention_relation_kl_b200 as rk
-from attention_relation_kl_b200 import _abi
+from attention_relation_kl_b200 import _abi, ops
 
 FAKE = 0x100000   # never dereferenced: every case fails its checks or has no work
 
@@ -147,3 +147,12 @@ def test_frequencies_follow_their_formulas():
 def test_bad_frequencies_are_refused(args):
     with pytest.raises(ValueError):
         rk.rotary_freqs(*args, device="cpu")
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        ops._on(torch.device("cuda", 0), Stream())
+    ops._on(torch.device("cuda", 1), Stream())       # entered by no one
