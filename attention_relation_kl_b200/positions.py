@@ -27,8 +27,8 @@ class RotaryFreqs(NamedTuple):
 
 
 def rotary_freqs(rot: int, base: float = 1e4, scaling: str = "none", factor: float = 1.0, *,
-                 original_length: int = 4096, low_turns: float = 1.0, high_turns: float = 32.0,
-                 device="cuda") -> RotaryFreqs:
+                 original_length: int = 4096, low_turns: float = 1.0,
+                 high_turns: Optional[float] = None, device="cuda") -> RotaryFreqs:
     """Frequencies f_i = base^(-2i/rot) of ``rot / 2`` pairs, scaled for contexts
     ``factor`` times as long as the ``original_length``:
 
@@ -38,13 +38,16 @@ def rotary_freqs(rot: int, base: float = 1e4, scaling: str = "none", factor: flo
     * ``"yarn"``: pairs that turn at least ``high_turns`` times within the original
       length keep f_i, those below ``low_turns`` take f_i / factor, with a ramp over
       the pairs between; the factor on the rotated entries is 0.1 ln(factor) + 1;
-    * ``"bands"``: as yarn, with the ramp over the number of turns, and no factor
-      (``high_turns=4`` is the usual choice with it).
+    * ``"bands"``: as yarn, with the ramp over the number of turns, and no factor.
+
+    Without ``high_turns`` it is 32 with yarn and 4 with bands, as is usual for them.
     """
     if rot < 0 or rot % 2:
         raise ValueError("rot must be even and not negative")
     if not (math.isfinite(base) and base > 1.0 and math.isfinite(factor) and factor > 0.0):
         raise ValueError("base must be above 1 and factor positive")
+    if high_turns is None:
+        high_turns = 4.0 if scaling == "bands" else 32.0
     if original_length < 1 or not 0.0 < low_turns < high_turns:
         raise ValueError("original_length must be positive and 0 < low_turns < high_turns")
     i = torch.arange(rot // 2, dtype=torch.float64)

@@ -156,3 +156,15 @@ def test_a_stream_of_another_device_is_refused():
     with pytest.raises(ValueError, match="stream is on cuda:1"):
         ops._on(torch.device("cuda", 0), Stream())
     ops._on(torch.device("cuda", 1), Stream())       # entered by no one
+
+
+def test_turns_that_bands_and_yarn_take_without_being_given():
+    get = lambda *a, **k: rk.rotary_freqs(128, 5e5, *a, original_length=8192, device="cpu", **k)  # noqa: E731
+    for kind, usual in (("bands", 4.0), ("yarn", 32.0)):
+        assert torch.equal(get(kind, 8.0).inv_freq, get(kind, 8.0, high_turns=usual).inv_freq)
+    # the published frequencies for bands: wavelengths from a quarter of the length to all of it
+    f = 5e5 ** (-2.0 * np.arange(64) / 128)
+    wave = 2 * np.pi / f
+    smooth = (8192 / wave - 1.0) / (4.0 - 1.0)
+    want = np.where(wave < 8192 / 4, f, np.where(wave > 8192, f / 8, (1 - smooth) * f / 8 + smooth * f))
+    assert np.allclose(get("bands", 8.0).inv_freq.numpy(), want, rtol=1e-14, atol=0)
