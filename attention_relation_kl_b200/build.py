@@ -14,6 +14,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -77,21 +78,27 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, checks: bool = False) -> str:
-    """Compile librelkl.so if any source is newer; returns its path.
+    """Compile librelkl.so if any source is newer; returns its path.  Then the
+    marshalling module, which needs Python's and torch's headers: where it cannot be
+    compiled there is a warning, and the loss, which does without, can be used.
 
     ``checks`` (or RELKL_CHECKS=1 in the environment) builds the debug variant
     that replays every tensor-core launch's schedule on the host first
     (relkl_check_schedule) and refuses a launch whose schedule is unsound."""
     checks = checks or os.environ.get("RELKL_CHECKS") == "1"
-    build_marshal(force, verbose)
-    if not force and not checks and not _stale():
-        return LIB
-    tmp = LIB + ".tmp"
-    cmd = [nvcc_path(), *NVCC_FLAGS, *(["-DRELKL_CHECKS"] if checks else []),
-           "-I", os.path.join(ROOT, "include"),
-           *[os.path.join(CSRC, f) for f in SOURCES], "-ldl", "-o", tmp]
-    _run(cmd, verbose)
-    os.replace(tmp, LIB)
+    if force or checks or _stale():
+        tmp = LIB + ".tmp"
+        cmd = [nvcc_path(), *NVCC_FLAGS, *(["-DRELKL_CHECKS"] if checks else []),
+               "-I", os.path.join(ROOT, "include"),
+               *[os.path.join(CSRC, f) for f in SOURCES], "-ldl", "-o", tmp]
+        _run(cmd, verbose)
+        os.replace(tmp, LIB)
+    try:
+        build_marshal(force, verbose)
+    except Exception as e:     # the library is whole without it; an old one may not fit it
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)
+        warnings.warn(f"the operators that need the marshalling module cannot be called: {e}")
     return LIB
 
 
