@@ -8,6 +8,7 @@ tree.  nvcc cross-compiles without a GPU.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -59,13 +60,27 @@ def _run(cmd, verbose: bool) -> None:
         raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
 
 
+def _torch() -> str:
+    """Which torch is installed, without importing it: its version, and where it is."""
+    where = importlib.util.find_spec("torch").submodule_search_locations[0]
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    return f"{version} {where}"
+
+
 def build_marshal(force: bool = False, verbose: bool = False) -> str:
-    """Compile the marshalling module if its sources are newer; returns its path."""
+    """Compile the marshalling module if its sources are newer, or if it was built for
+    another torch (which stands in a file beside it); returns its path."""
     deps = [MARSHAL_SOURCE, os.path.join(CSRC, "relkl_ranges.h"), os.path.join(ROOT, "include", "relkl.h"),
             __file__]
-    if not force and os.path.exists(MARSHAL) and \
+    record, torch_now = MARSHAL + ".torch", _torch()
+    if not force and os.path.exists(MARSHAL) and os.path.exists(record) and \
             all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
-        return MARSHAL
+        with open(record) as f:
+            if f.read() == torch_now:
+                return MARSHAL
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     tmp = MARSHAL + ".tmp"
@@ -74,6 +89,8 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
           "-I", sysconfig.get_paths()["include"], MARSHAL_SOURCE, "-L", lib, f"-Wl,-rpath,{lib}",
           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-o", tmp], verbose)
     os.replace(tmp, MARSHAL)
+    with open(record, "w") as f:
+        f.write(torch_now)
     return MARSHAL
 
 

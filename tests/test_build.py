@@ -49,3 +49,19 @@ def test_a_library_that_cannot_be_built_is_an_error(compilers):
     with pytest.raises(RuntimeError, match="nvcc"):
         b.build()
     assert ran == []
+
+
+def test_the_module_is_built_again_for_another_torch(compilers, monkeypatch):
+    ran, _ = compilers
+    b.build()
+    b.build()
+    assert ran == ["nvcc", "g++"]
+    real = b.importlib.metadata.version
+    monkeypatch.setattr(b.importlib.metadata, "version", lambda name: real(name) + ".other")
+    b.build()
+    assert ran == ["nvcc", "g++", "g++"]
+    b.build()
+    assert ran == ["nvcc", "g++", "g++"]
+    os.remove(b.MARSHAL + ".torch")          # one that says nothing of it
+    b.build()
+    assert ran == ["nvcc", "g++", "g++", "g++"]
