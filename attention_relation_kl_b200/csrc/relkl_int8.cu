@@ -1186,7 +1186,8 @@ cudaError_t gemv(const GemvParams& p, int num_sms, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   // the most that any call takes, not this one's: the limit is the process's, and
   // another thread's launch may come between a smaller one and its own
-  if (smem > 48 * 1024)
+  constexpr int fixed = R * (GEMV_THREADS / 32 + 1) * 4;   // the kernel's part[] and largest_of[]
+  if (smem + fixed > 48 * 1024)
     e = cudaFuncSetAttribute(relkl_gemv_i8_kernel<T, U, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemvBytes);
   if (e != cudaSuccess) return e;
   // as many CTAs as the SMs hold at a time: more would code the rows once more

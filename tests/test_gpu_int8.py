@@ -368,3 +368,13 @@ def test_few_long_rows_from_two_threads():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+# codes just below, at and above 48 KB, where a block's own shared memory counts too
+@pytest.mark.parametrize("rows,K", [(4, 12288), (4, 12272), (4, 12208), (4, 12304), (3, 16384), (3, 16320), (2, 24576),
+                                    (2, 24500), (1, 49152), (1, 49088), (1, 49100), (1, 98304)])
+def test_few_rows_around_the_default_limit_of_shared_memory(rows, K):
+    w, sw = _weights(24, K, 3)
+    x = _randn((rows, K), BF16, 4)
+    q, sx = _codes(x)
+    _check(rk.relkl_linear_i8(x, w, sw, out_dtype=F32), q, sx, w, sw)
