@@ -1291,12 +1291,21 @@ cudaError_t gemm_pair(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
 // waves of tiles times the time of one wave, as measured (K = 4096, full
 // waves: 9.3 us with one CTA and 64 columns, 11.0 with 128; pairs 8.5 with 128
 // columns, 11.3 with 256; a single wave 10.9, 11.6, 11.6 and 15.0 us, so that
-// pairs with 128 are counted as 9.5).  128 and 256 rows x 4096 channels take 64
-// columns a tile (10.4 and 11.0 us; the others 11.6 to 15), 500 rows pairs with
-// 128 (12.3; 64 columns 20.6, pairs with 256 15.3), 1000 rows pairs with 256
-// (16.3; 38, 23 and 20).  Where tiles of 64 columns leave SMs idle, K is split
-// over up to four of them: 16 rows x 1024 channels 10.0 us alone, 8.9 and 6.9 us
-// with two and four shares, 11.3 us with eight.
+// pairs with 128 are counted as 9.5).  K = 4096, 4096 channels, weights from HBM:
+// 128 and 256 rows take 64 columns a tile (12.4 and 11.9 us; the others 12.8 to
+// 16.2), 500 rows pairs with 128 (13.5; one CTA with 128 13.1, with 64 21.6), 1000
+// rows pairs with 256 (16.9; 39.7, 23.8 and 21.0).  The same weights for every K:
+// at K of 256, 512 and 1024 (16 to 16384 rows, 1024 and 4096 channels) the choice
+// was the fastest of the four or within 12 % of it (1000 x 512 x 4096 8.0 us,
+// pairs with 128 7.2).
+//
+// Where tiles of 64 columns leave SMs idle, K is split over two or four of them.
+// The shares' sums meet in shared memory, which costs as much as some 16 chunks
+// of K: 77 rows x 1024 channels with one, two and four shares at K = 1024 4.7, 7.0
+// and 6.6 us, 2048 6.7, 8.0 and 7.2, 2560 8.2, 9.0 and 7.9, 4096 10.7, 10.4 and 8.6,
+// 8192 17.7, 14.1 and 10.5.  So four shares from 20 chunks on, and two, where four
+// are too many for the SMs, from 32 (77 rows x 4096 channels: one and two at 2560
+// 8.5 and 9.9, 4096 11.3 and 11.7, 8192 18.7 and 15.6; 9 rows at 4096 11.2 and 10.9).
 template <typename U>
 cudaError_t gemm_pick(I8Params& p, const I8Call& c, int num_sms, cudaStream_t stream) {
   p.k_chunks = (c.K + i8::BK - 1) / i8::BK;
@@ -1311,7 +1320,10 @@ cudaError_t gemm_pick(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
   const int64_t least = std::min(std::min(one64, one128), std::min(two128, two256));
   if (two256 == least) return gemm_pair<256, U>(p, c, num_sms, stream);
   if (one64 == least) {
-    while (p.split < 4 && t64 * p.split * 2 <= num_sms && p.k_chunks >= p.split * 8) p.split *= 2;
+    if (t64 * 4 <= num_sms && p.k_chunks >= 20)
+      p.split = 4;
+    else if (t64 * 2 <= num_sms && p.k_chunks >= 32)
+      p.split = 2;
     return gemm<64, U>(p, c, stream);
   }
   if (two128 == least) return gemm_pair<128, U>(p, c, num_sms, stream);

@@ -165,9 +165,18 @@ struct NormParams {
 
 // Products in 8-bit integers: row codes, few rows, and the tensor-core product.
 // Most rows of the kernel for few rows.  Against the tensor cores (coding and
-// product, the second started early), K x channels: 4096 x 4096, 1, 2, 4 and 5
-// rows 4.9, 6.3, 9.4 and 10.8 us, there 9.9 us; 1024 x 1024, 4 rows 5.0, there
-// 7.2; 8192 x 8192, 2, 4 and 5 rows 13, 21 and 28, there 19 us.
+// product, the second started early), us with 1, 2, 3 and 4 rows, weights from HBM:
+//   K x channels   here                     there
+//   1024 x 1024    2.5, 3.3, 4.2, 4.9       7.0
+//   4096 x 1024    6.0, 6.9, 7.8, 9.0       7.9
+//   4096 x 4096    7.6, 8.7, 10.2, 11.5     11.5
+//   8192 x 8192    21.7, 24.1, 26.6, 29.2   20.6
+//   4096 x 16384   18.9, 20.8, 22.6, 24.5   17.1
+//   16384 x 4096   23.0, 26.2, 29.6, 33.2   23.5
+// Five and six rows take longer than there from 4096 x 1024 on (10.1 and 11.1).
+// Above 16 M weights it is behind by up to 45 % where these come from HBM; from L2 it
+// is ahead up to two rows there too (8192 x 8192 10.3 and 13.2, there 17.9).  The
+// limit does not look at the channels, as a caller asks for scratch by rows and K.
 constexpr int kGemvRows = 4;
 constexpr int kGemvBytes = 96 * 1024; // most bytes of their codes in shared memory
 

@@ -378,3 +378,15 @@ def test_few_rows_around_the_default_limit_of_shared_memory(rows, K):
     x = _randn((rows, K), BF16, 4)
     q, sx = _codes(x)
     _check(rk.relkl_linear_i8(x, w, sw, out_dtype=F32), q, sx, w, sw)
+
+
+# sums by one, two and four CTAs of a cluster: the limits' both sides, shares of unequal length,
+# and tiles at the rows' and the channels' end
+@pytest.mark.parametrize("rows,cols,K", [(77, 1000, 2432), (77, 1000, 2433), (9, 2370, 3968), (9, 2370, 4100),
+                                         (300, 900, 3968), (300, 900, 4500), (129, 2300, 8000)])
+@pytest.mark.parametrize("yt", [BF16, F32])
+def test_shares_of_a_split_sum(rows, cols, K, yt):
+    x = _randn((rows, K), BF16, 6)
+    w, sw = _weights(cols, K)
+    q, sx = _codes(x)
+    _check(rk.relkl_linear_i8(x, w, sw, out_dtype=yt), q, sx, w, sw)
