@@ -172,7 +172,10 @@ PyObject* adamw(PyObject*, PyObject* args) {
     const Items steps(one_step ? ps : ns, "step must be a number or a sequence");
     if (steps.size() != n) raise(PyExc_ValueError, "step needs one number, or one for each tensor");
     int index = -1;
-    std::map<std::pair<bool, long long>, std::vector<relkl_adamw_tensor>> groups;   // by (8 bits, step)
+    using Key = std::pair<bool, long long>;      // 8 bits, step
+    std::map<Key, std::vector<relkl_adamw_tensor>> groups;
+    std::vector<relkl_adamw_tensor>* group = nullptr;   // that of the last tensor, whose key is
+    Key last;
     for (Py_ssize_t k = 0; k < n; ++k) {
       const at::Tensor& p = tensor(params[k], "params");
       const at::Tensor& g = tensor(grads[k], "gradients");
@@ -227,9 +230,13 @@ PyObject* adamw(PyObject*, PyObject* args) {
         raise(PyExc_ValueError, "float32 states have no scales");
       }
       r.weight_decay = static_cast<float>(one_decay ? decay : number(decays[k]));
-      auto& group = groups[{bits8, one_step ? step : whole(steps[k])}];
-      if (groups.size() == 1 && group.empty()) group.reserve(static_cast<size_t>(n));
-      group.push_back(r);
+      const Key key{bits8, one_step ? step : whole(steps[k])};
+      if (!group || key != last) {
+        group = &groups[key];
+        last = key;
+        if (groups.size() == 1) group->reserve(static_cast<size_t>(n));
+      }
+      group->push_back(r);
     }
     if (groups.size() > 1) {   // as many calls, each of which looks at its own arrays
       std::vector<relkl::Range> ranges(relkl::kAdamwRanges * static_cast<size_t>(n));

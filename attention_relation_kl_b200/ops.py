@@ -99,9 +99,10 @@ class _on:
     a stream that was not asked for, under the wrong device."""
 
     def __init__(self, device: torch.device, stream=None):
-        where = getattr(stream, "device", None)
-        if isinstance(where, torch.device) and where != device:
-            raise ValueError(f"stream is on {where}, the tensors are on {device}")
+        if stream is not None:
+            where = getattr(stream, "device", None)
+            if isinstance(where, torch.device) and where != device:
+                raise ValueError(f"stream is on {where}, the tensors are on {device}")
         self.device, self.stream, self.inner = device, stream, None
 
     def __enter__(self) -> int:

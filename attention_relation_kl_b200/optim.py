@@ -83,19 +83,18 @@ def relkl_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         step_ptr = _scalar(step_dev, torch.int64, index, "step")
     if grad_scale is not None:
         scale_ptr = _scalar(grad_scale, torch.float32, index, "grad_scale")
-    lib, status, calls = _abi.lib(), _abi.RELKL_OK, 0
+    lib, launched = _abi.lib(), 0
     with _on(params[0].device, stream) as handle:
-        plans = [_PLAN.pack(bits, 0, lr, betas[0], betas[1], eps, number, lr_ptr, step_ptr, scale_ptr)
-                 for bits, number, _, _ in groups]
-        if len(groups) > 1:        # all are refused, or none
-            for (_, _, n, table), plan in zip(groups, plans):
-                check(lib.relkl_adamw_check(n, table, plan), "relkl_adamw")
-        for (_, _, n, table), plan in zip(groups, plans):
+        for bits, number, n, table in groups if len(groups) > 1 else ():    # all are refused, or none
+            plan = _PLAN.pack(bits, 0, lr, betas[0], betas[1], eps, number, lr_ptr, step_ptr, scale_ptr)
+            check(lib.relkl_adamw_check(n, table, plan), "relkl_adamw")
+        for bits, number, n, table in groups:
+            plan = _PLAN.pack(bits, 0, lr, betas[0], betas[1], eps, number, lr_ptr, step_ptr, scale_ptr)
             status = lib.relkl_adamw(n, table, plan, handle)
             if status != _abi.RELKL_OK:
                 break
-            calls += 1
-    if calls or status == _abi.RELKL_ERR_CUDA:     # something may have been written
+            launched += 1
+    if launched or status == _abi.RELKL_ERR_CUDA:     # something may have been written
         _abi.marshal().written(params)
         if copies is not None:
             _abi.marshal().written(copies)
@@ -172,16 +171,19 @@ class AdamW:
         pick = lambda xs: [xs[k] for k in at]  # noqa: E731
         grads = pick(grads)
         clip = None if self.max_norm is None else relkl_grad_norm(grads, self.max_norm)
-        counts = [self.counts[k] + 1 for k in at]
-        if counts.count(counts[0]) == len(counts):
-            counts = counts[0]
-        relkl_adamw(pick(self.params), grads, pick(self.state), lr=self.lr, step=counts,
+        counts, n = self.counts, len(self.params)
+        even = counts.count(counts[0]) == n
+        step = counts[0] + 1 if even else [counts[k] + 1 for k in at]
+        relkl_adamw(pick(self.params), grads, pick(self.state), lr=self.lr, step=step,
                     betas=self.betas, eps=self.eps, weight_decay=pick(self.weight_decay),
                     copies=None if self.copies is None else pick(self.copies),
                     grad_scale=None if clip is None else clip[1:])
         self._steps += 1
-        for k in at:
-            self.counts[k] += 1
+        if even and len(at) == n:
+            self.counts = [step] * n
+        else:
+            for k in at:
+                counts[k] += 1
         return None if clip is None else clip[0]
 
     def state_dict(self) -> dict:
