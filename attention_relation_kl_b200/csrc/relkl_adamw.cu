@@ -12,14 +12,15 @@
 // never as zero, so that no element's step is divided by eps alone.  p is
 // updated from the new m and v before they are rounded to codes.
 //
-// What bounds it: HBM.  Every byte is read once and written once (28 to 30 B
-// an element with float32 states and weights, 16 to 18 with 8-bit states), all
-// tensors of a call go in one launch (their table travels in the kernel's
+// What bounds it: HBM.  Every byte is read once and written once (26 to 30 B
+// an element with float32 states and weights, by the gradient's type and the
+// copies, and 14 to 18 with 8-bit states; bf16 weights and gradients 22 and 10),
+// all tensors of a call go in one launch (their table travels in the kernel's
 // parameters, so a captured graph needs no memory of its own for it), and the
 // statistics of an 8-bit block stay in the registers of its warp.
 //
 // Measured (B200, copy bandwidth 6.56 TB/s), 201 M float32 weights with bf16
-// copies and gradients: float32 states 823 us, 6.8 TB/s; 8-bit states 500 us, 6.5
+// copies and gradients: float32 states 824 us, 6.8 TB/s; 8-bit states 492 us, 6.6
 // TB/s.  The 8-bit step is close to the issue rate too: with correctly rounded
 // roots and quotients (99 instructions an element) it took 693 us in an earlier
 // form, with one block for a warp 536 us, and with a lane's eight elements next to
@@ -496,9 +497,13 @@ __device__ __forceinline__ double square(float x) {
 }
 
 // A chunk: consecutive elements of one tensor, of which a thread holds four
-// accesses of 16 bytes (a warp's are next to one another).  201 M elements take
-// 84 us in bf16 and 145 us in float32, 5.3 and 5.9 TB/s with 5 us of launches;
-// with eight elements to a thread at a time, in accesses whose halves of sectors
+// accesses of 16 bytes (a warp's are next to one another).  201 M elements from
+// HBM take 84 to 87 us in bf16 and 145 to 147 us in float32, 4.7 and 5.5 TB/s, of
+// which some 7 us are a graph's start and the two launches (5.1 and 5.8 TB/s
+// without them); where the end of the gradients is still in L2, 63 and 116 us.
+// What holds bf16 at 1.3 times its bytes' time is not known.  A thread one of whose four
+// accesses sums up to less than 1e-30, as zeros do, reads and sums them again: with
+// every other row zero 105 and 160 us instead of 63 and 116.  With eight elements to a thread at a time, in accesses whose halves of sectors
 // came twice, 129 and 190 us.  256 threads a CTA, two or eight accesses, or the
 // next chunk's loads before this one's sums: 85 to 98 and 145 to 168 us.
 struct Chunk {
@@ -634,7 +639,10 @@ cudaError_t adamw_group(const AdamwTensor* t, int n, const AdamwPlan& plan, cuda
 // Elements from which a warp takes two 8-bit blocks.  It loads both before it
 // works on the first, and looks up tensor and scalars once: 201 M elements take
 // 500 us instead of 536 (float32 weights, bf16 gradients and copies), 406
-// instead of 465 (all bf16), 485 instead of 521 (all float32).  Fewer fill the
+// instead of 465 (all bf16), 485 instead of 521 (all float32).  Seven CTAs an SM
+// leave 72 registers, and 30 words spill: 491, 404 and 474 us; with 8 CTAs 488,
+// 397 and 502, with 6 516, 421 and 486, with 5, where nothing spills, 547, 480 and
+// 528.  Fewer fill the
 // SMs worse that way: 34 M 96, 74, 94 and 94, 82, 96 us, 12.6 M 47, 33, 47 and 41,
 // 37, 45, 3.1 M 25, 14, 25 and 16, 14, 18.
 constexpr int64_t kAdamwTwoBlocks = int64_t(1) << 25;

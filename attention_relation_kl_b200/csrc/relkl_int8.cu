@@ -9,17 +9,20 @@
 //
 // Four kernels:
 //   * relkl_quantize_rows_kernel: one pass over the rows.  HBM: 32K x 4096 bf16
-//     in 61 to 68 us, 6.6 to 5.9 TB/s.
+//     in 61 to 70 us, 6.6 to 5.7 TB/s.
 //   * relkl_gemv_i8_kernel, up to kGemvRows rows: every CTA codes the rows for
 //     itself in shared memory (they are small and in L2) while its warps'
 //     weights are on the way, then one warp per channel sums with dp4a.  Bound
-//     by the launch and the weights' bytes: 1 x 4096 x 4096 in 4.8 us.
+//     by the launch and the weights' bytes: 1 x 4096 x 4096 in 4.7 us where they are
+//     in L2, 7.6 us from HBM.
 //   * relkl_gemm_i8_kernel: tcgen05.mma kind::i8 (s8 x s8 -> s32) with both
 //     operands K-major in 128-byte swizzled shared memory, fed by TMA; one tile
 //     for a CTA, or K split over a cluster, for tens to hundreds of rows.
 //   * relkl_gemm_i8_pair_kernel: the same by pairs of CTAs, persistent.  32K x
-//     4096 x 4096 in 337 us, 3.27 POP/s (99 % of twice the measured bf16 rate);
-//     a library product of the same codes to int32, without scales, takes 341.
+//     4096 x 4096 in 328 to 337 us, 3.35 to 3.27 POP/s, as long as the GPU is not
+//     limited by its power (twice the measured bf16 burst rate is 3.31); after some
+//     seconds 399 us.  A library product of the same codes to int32, without scales,
+//     takes 336 and 390.  With the coding a call takes 387 us, after some seconds 456.
 #include <algorithm>
 #include <cstdint>
 
@@ -810,11 +813,11 @@ relkl_gemm_i8_kernel(const __grid_constant__ I8Params p) {
 // 128 rows of q and half of the channels' codes, so an SM reads (128 + BN / 2)
 // x 32 bytes of shared memory for an instruction where one CTA by itself reads
 // (128 + BN) x 32; at the int8 rate the latter needs more than the 128 bytes a
-// clock that an SM has (32K x 4096 x 4096: 936 us with its coding, then 437).
+// clock that an SM has (32K x 4096 x 4096 with its coding: 936 us, then 437).
 // Persistent; the sums of one tile are read from TMEM while the next one's are
 // formed.  What the tiles fetch from L2, 15 TB/s, is next to bound it: results
 // that left lane by lane (32 bytes of a row each) cost 372 us, as whole lines
-// by TMA 337.
+// by TMA 337 at the same clock.
 namespace i8 {
 
 // warp 0 TMA, warp 1 MMA, warps 2-9 epilogue: two for each quarter of the

@@ -14,13 +14,17 @@
 // of its few pairs of one token in registers and runs over the heads of a
 // group with them; no table is read or written.
 //
-// Measured (B200, copy bandwidth 6.56 TB/s): 32K tokens, Q, K and V of 32
-// heads of 128, bf16, tokens to heads: 273 us, 5.9 TB/s; gradients of 2 x 16K
-// tokens, 32 + 8 + 8 heads, fp32 heads to bf16 tokens: 182 us, 6.6 TB/s.  What
-// made the difference was how many rows are in flight, not how many bytes a
-// thread has: one head at a time at 8 blocks an SM (32 registers) against four
-// heads at 3 blocks: 285 and 321 us; loads past L1 against streaming ones: 273
-// and 279 us (182 and 193 us for the gradients).
+// Measured (B200, copy bandwidth 6.56 TB/s; on the GPU, by a replayed graph):
+// 32K tokens, Q, K and V of 32 heads of 128, bf16, tokens to heads: 269 us, 6.0
+// TB/s; gradients of 2 x 16K tokens, 32 + 8 + 8 heads, fp32 heads to bf16
+// tokens: 182 us, 6.7 TB/s.  What made the difference was how many rows are in
+// flight, not how many bytes a thread has: one head at a time at 8 blocks an SM
+// against four heads at 3 blocks: 285 and 321 us; loads past L1 against streaming
+// ones: 273 and 279 us (182 and 193 us for the gradients).  8 blocks leave a
+// thread 32 registers, in which half of the variants spill (bf16 in both, halves,
+// 8 entries wide, which the 32K inputs take, 60 bytes stored and 72 loaded before
+// the loop over heads); with 6, 5 and 4 blocks they took 280, 297 and 332 us, the
+// gradients 202, 221 and 246.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -34,8 +38,10 @@ namespace {
 
 // m cos(pos f) and m sin(pos f).  The angle is reduced by whole turns in
 // double precision, in units of pi; its float part goes through sincospif and
-// the rest enters by the first-order term, so both are good to an ulp of 1 at
-// any position whose angle a double can hold.
+// the rest enters by the first-order term, so both are off by an ulp of 1 at
+// most, and by what the angle itself is off: its position, two products and 1 /
+// pi round, 4 * 2^-53 of the angle, which reaches that ulp at angles of 2^27
+// (past a position of 10^8 for the fastest pair).
 __device__ __forceinline__ void pair_angle(double pos, double f, float m, float& c, float& s) {
   const double u = pos * f * 0.31830988618379067154;   // half turns: angle / pi
   const double r = fma(-2.0, rint(0.5 * u), u);        // exact, in [-1, 1]
@@ -260,8 +266,9 @@ cudaError_t launch(RotaryParams& p, int num_sms, cudaStream_t stream) {
   }
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   // As many heads for one thread as leave the SMs two waves of blocks, but at
-  // most 4: with 1, 2, 4, 8, 16 heads the 32K inputs took 493, 319, 279, 285,
-  // 289 us (angles weigh on the left, distant rows in flight on the right).
+  // most 4: with 1, 2, 4, 8, 16 heads the 32K inputs took 520, 326, 269, 272,
+  // 271 us, the gradients 367, 219, 182, 181, 181 (angles weigh on the left; on
+  // the right nothing is gained, and fewer blocks fill the last wave worse).
   int64_t hg = work / (static_cast<int64_t>(num_sms) * 16);
   hg = hg < 1 ? 1 : (hg > 4 ? 4 : hg);
   while ((most + hg - 1) / hg * p.n > 65535) hg *= 2;   // the grid's y extent

@@ -30,7 +30,7 @@ def teacher_relations_i8(h_t: torch.Tensor, weights: Dict[str, Sequence[torch.Te
     B, N, D = h_t.shape
     # Few tokens are coded by the kernel that multiplies them; more are coded once for all
     # relations: 32768 x 4096 tokens through 32, 8 and 8 heads of 128 and the rotation take
-    # 722 us, coded for each relation 855.
+    # 700 us on the GPU, coded for each relation 825.
     codes = None
     if len(weights) > 1 and _abi.lib().relkl_linear_i8_bytes(B * N, D) > 0:
         codes = relkl_quantize_rows(h_t)

@@ -158,8 +158,10 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, *, positions: Optional[torch
            out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """Differentiable relkl_rotary (the frequencies and positions get no gradient).
 
-    Its backward pass may be captured into a graph once no eager graph of the same leaves,
-    made on another stream, is alive; until then it is refused."""
+    It has a backward pass, itself differentiable, and no forward-mode derivative or rule for
+    torch.func's transforms, which refuse it.  The backward pass may be captured into a graph
+    once no eager graph of the same leaves, made on another stream, is alive; until then it
+    is refused."""
     args = dict(pos_scale=pos_scale, pos_offset=pos_offset, mscale=mscale, interleaved=interleaved,
                 inverse=bool(inverse))
     return Rotary.apply(x, inv_freq, positions, args, out_dtype)

@@ -399,8 +399,10 @@ relkl_status relkl_rotary(int32_t n_tensors, const relkl_rotary_tensor* tensors,
  * consecutive elements times its scale in m_scale / v_scale,
  * float [ceil(n / 256)]: the block's largest magnitude / 448 (0 where that is
  * below 2^-126; the block's codes are then 0).  A positive root is never held
- * as 0 in a block that has a scale: it takes the smallest code.  A fresh state
- * is zeros throughout, in either form.                                       */
+ * as 0 in a block that has a scale: it takes the smallest code.  A NaN or an
+ * infinity in a block's moments is in its scale, and so in the whole block's
+ * moments from the next step on.  A fresh state is zeros throughout, in either
+ * form.                                                                      */
 typedef struct {
   const void* grad;      /* in, grad_dtype                                    */
   void* param;           /* in and out, param_dtype                           */
@@ -474,8 +476,9 @@ relkl_status relkl_grad_norm(int32_t n_tensors, const relkl_norm_tensor* tensors
  *
  *   y[r, c] = q_scale[r] w_scale[c] sum_k q[r, k] w[c, k] + bias[c]
  *
- * The sum is exact in int32 (0 < K < 131072); it is rounded to float32, scaled,
- * and rounded once to y's type.  Code arrays (q, w) are int8 row-major with a
+ * The sum is exact in int32 (0 < K < 131072); it is rounded to float32, multiplied
+ * with the float32 product of the two scales (which has to be in float32's range, or
+ * y is not the formula's), and rounded once to y's type.  Code arrays (q, w) are int8 row-major with a
  * row stride in bytes that is a multiple of 16 and at least K, at 16-byte
  * aligned addresses; what lies between K and the stride is not read.  x and y
  * are row-major with any stride of at least K (cols) elements, at addresses

@@ -360,3 +360,13 @@ def test_outputs_are_written_once():
     q = _randn((1, 4, 9, 64), F32, 2)
     with pytest.raises(RuntimeError, match="INVALID"):     # a layer that shares K and V
         rk.relkl_rotary_qkv([q, x, x], f, apply=(True, True, False), out=[q, x, x])
+
+
+def test_transforms_without_a_rule_are_refused():
+    x, f = _randn((1, 2, 5, 64), F32), rk.rotary_freqs(64).inv_freq
+    with pytest.raises(RuntimeError):
+        torch.func.vmap(lambda z: rk.rotary(z, f))(x[None])
+    with pytest.raises(RuntimeError):
+        torch.func.grad(lambda z: rk.rotary(z, f).sum())(x)
+    with pytest.raises(RuntimeError), torch.autograd.forward_ad.dual_level():
+        rk.rotary(torch.autograd.forward_ad.make_dual(x, torch.ones_like(x)), f)
