@@ -1303,12 +1303,13 @@ cudaError_t gemm_pair(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
 // pairs with 128 7.2).
 //
 // Where tiles of 64 columns leave SMs idle, K is split over two or four of them.
-// The shares' sums meet in shared memory, which costs as much as some 16 chunks
-// of K: 77 rows x 1024 channels with one, two and four shares at K = 1024 4.7, 7.0
-// and 6.6 us, 2048 6.7, 8.0 and 7.2, 2560 8.2, 9.0 and 7.9, 4096 10.7, 10.4 and 8.6,
-// 8192 17.7, 14.1 and 10.5.  So four shares from 20 chunks on, and two, where four
-// are too many for the SMs, from 32 (77 rows x 4096 channels: one and two at 2560
-// 8.5 and 9.9, 4096 11.3 and 11.7, 8192 18.7 and 15.6; 9 rows at 4096 11.2 and 10.9).
+// The shares' sums meet in shared memory, which costs as much as some chunks of K
+// and one more for each 8 rows of a tile.  One share and four, 1024 channels,
+// weights from HBM: 5 rows at K = 1280 5.0 and 5.1 us, 1536 5.4 and 5.2; 32 rows 1536
+// 5.5 and 5.7, 1792 6.1 and 6.0; 77 rows 2304 7.4 and 7.7, 2560 8.1 and 7.9, 4096 10.8
+// and 8.6; 128 rows 2560 8.3 and 9.0, 3584 10.0 and 9.7.  One and two, where four
+// are more than the SMs (4096 channels): 5 rows at 3584 10.1 and 10.3, 4096 11.2 and
+// 10.9; 32 rows 4096 11.2 and 11.1; 77 rows 4096 11.3 and 11.5, 8192 18.7 and 15.6.
 template <typename U>
 cudaError_t gemm_pick(I8Params& p, const I8Call& c, int num_sms, cudaStream_t stream) {
   p.k_chunks = (c.K + i8::BK - 1) / i8::BK;
@@ -1323,9 +1324,10 @@ cudaError_t gemm_pick(I8Params& p, const I8Call& c, int num_sms, cudaStream_t st
   const int64_t least = std::min(std::min(one64, one128), std::min(two128, two256));
   if (two256 == least) return gemm_pair<256, U>(p, c, num_sms, stream);
   if (one64 == least) {
-    if (t64 * 4 <= num_sms && p.k_chunks >= 20)
+    const int meet = static_cast<int>(std::min<int64_t>(p.rows, i8::BM)) / 8;
+    if (t64 * 4 <= num_sms && p.k_chunks >= 12 + meet)
       p.split = 4;
-    else if (t64 * 2 <= num_sms && p.k_chunks >= 32)
+    else if (t64 * 2 <= num_sms && p.k_chunks >= 28 + meet)
       p.split = 2;
     return gemm<64, U>(p, c, stream);
   }

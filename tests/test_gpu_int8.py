@@ -383,7 +383,9 @@ def test_few_rows_around_the_default_limit_of_shared_memory(rows, K):
 # sums by one, two and four CTAs of a cluster: the limits' both sides, shares of unequal length,
 # and tiles at the rows' and the channels' end
 @pytest.mark.parametrize("rows,cols,K", [(77, 1000, 2432), (77, 1000, 2433), (9, 2370, 3968), (9, 2370, 4100),
-                                         (300, 900, 3968), (300, 900, 4500), (129, 2300, 8000)])
+                                         (300, 900, 3968), (300, 900, 4500), (129, 2300, 8000),
+                                         (77, 1000, 2560), (77, 1000, 2561), (9, 2370, 3585), (9, 2370, 3584),
+                                         (8, 64, 1540), (5, 64, 1537), (5, 130, 1536), (300, 900, 5600)])
 @pytest.mark.parametrize("yt", [BF16, F32])
 def test_shares_of_a_split_sum(rows, cols, K, yt):
     x = _randn((rows, K), BF16, 6)
